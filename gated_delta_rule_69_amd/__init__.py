@@ -16,6 +16,10 @@ torchtitan (training)", quoted attention-gym description):
   chunk_kda_bwd   steps B1..B3 (kda_chunk_bwd)
   recurrent_kda   step A7  (kda_recurrent_fwd); with use_gate_in_kernel=True
                   steps A1 + A7 (kda_recurrent_fwd_fused_gate)
+and, for layers whose gate is one number per value head and token, and for the
+output norm behind either scan:
+  chunk_gdn, chunk_gdn_bwd, recurrent_gdn   the scalar-gate scan (gdn.py)
+  gated_norm, gated_norm_bwd                the (gated) output norm (norm.py)
 """
 from __future__ import annotations
 
@@ -39,7 +43,9 @@ EXPORTED = ("kda_status_string", "kda_gate_cumsum", "kda_gate_cumsum_biased",
             "kda_chunk_fwd_ex", "kda_recurrent_fwd_ex", "kda_chunk_fwd_conv", "kda_short_conv_fwd",
             "kda_recurrent_fwd_conv_workspace_bytes", "kda_recurrent_fwd_conv",
             "kda_recurrent_fwd_conv_noalloc", "kda_chunk_fwd_train", "kda_chunk_bwd_saved",
-            "kda_chunk_fwd_train_ex", "kda_chunk_bwd_ex")
+            "kda_chunk_fwd_train_ex", "kda_chunk_bwd_ex", "kda_gdn_chunk_workspace_bytes",
+            "kda_gdn_chunk_fwd", "kda_gdn_chunk_bwd", "kda_gdn_recurrent_fwd", "kda_norm_fwd",
+            "kda_norm_bwd_workspace_bytes", "kda_norm_bwd")
 # bytes of the library's static device scratch behind kda_recurrent_fwd_conv_noalloc
 NOALLOC_SCRATCH_BYTES = 16 << 20
 KDA_GATE_LOG2, KDA_GATE_NAT, KDA_GATE_RAW = 0, 1, 2
@@ -130,6 +136,21 @@ def _lib():
         lib.kda_recurrent_fwd_conv_noalloc.argtypes = [dims, ctypes.c_int, p, p, p, conv, p, p, p, i32,
                                                        p, i32, p, p, p, i32, p, p, p]
         lib.kda_recurrent_fwd_conv_noalloc.restype = ctypes.c_int
+        lib.kda_gdn_chunk_workspace_bytes.argtypes = [dims, ctypes.c_int, i32]
+        lib.kda_gdn_chunk_workspace_bytes.restype = sz
+        lib.kda_gdn_chunk_fwd.argtypes = [dims, ctypes.c_int, p, p, p, p, i32, p, p, p, i32, p, p, p, sz, p]
+        lib.kda_gdn_chunk_fwd.restype = ctypes.c_int
+        lib.kda_gdn_chunk_bwd.argtypes = ([dims, ctypes.c_int, p, p, p, p, i32] + [p] * 14 + [sz, p])
+        lib.kda_gdn_chunk_bwd.restype = ctypes.c_int
+        lib.kda_gdn_recurrent_fwd.argtypes = [dims, ctypes.c_int, p, p, p, p, i32, p, p, p, i32, p, p, p]
+        lib.kda_gdn_recurrent_fwd.restype = ctypes.c_int
+        i64 = ctypes.c_int64
+        lib.kda_norm_fwd.argtypes = [ctypes.c_int, i64, p, p, i32, i32, p, p, p, p]
+        lib.kda_norm_fwd.restype = ctypes.c_int
+        lib.kda_norm_bwd_workspace_bytes.argtypes = [p]
+        lib.kda_norm_bwd_workspace_bytes.restype = sz
+        lib.kda_norm_bwd.argtypes = [ctypes.c_int, i64, p, p, i32, i32] + [p] * 8 + [sz, p]
+        lib.kda_norm_bwd.restype = ctypes.c_int
         _LIB = lib
     return _LIB
 
@@ -662,3 +683,7 @@ def recurrent_kda(q, k, v, gate, beta, initial_state=None, *, cu_seqlens=None,
 __all__ = ["gate_cumsum", "chunk_kda", "chunk_kda_bwd", "recurrent_kda", "short_conv", "conv_state_shape",
            "chunk_workspace_bytes", "load",
            "KdaDims", "KdaShortConv", "KdaError", "LIB_PATH", "EXPORTED", "KDA_FP32", "KDA_BF16"]
+
+
+from .gdn import chunk_gdn, chunk_gdn_bwd, chunk_gdn_workspace_bytes, recurrent_gdn  # noqa: E402,F401
+from .norm import gated_norm, gated_norm_bwd  # noqa: E402,F401

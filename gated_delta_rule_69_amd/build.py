@@ -16,7 +16,8 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libkda.so")
 OBJDIR = os.path.join(os.path.dirname(HERE), "_build", "libkda")
 SOURCES = ["kda_api.hip", "kda_gate.hip", "kda_recurrent.hip", "kda_conv.hip", "kda_chunk.hip",
-           "kda_chunk_bwd.hip"]
+           "kda_chunk_bwd.hip", "kda_gdn_chunk.hip", "kda_gdn_chunk_bwd.hip", "kda_gdn_recurrent.hip",
+           "kda_norm.hip"]
 ARCH = "gfx950"
 
 

@@ -4,6 +4,8 @@
 #include <mutex>
 
 #include "kda_common.h"
+#include "kda_gdn.h"
+#include "kda_norm.h"
 
 // Scratch of kda_recurrent_fwd_conv_noalloc: device memory the library owns, so
 // that callers that cannot allocate (graph capture, serving loops) need not
@@ -610,6 +612,224 @@ kda_status kda_recurrent_fwd_ex(const kda_dims* d, kda_dtype dt, const void* q, 
   if (gate_kind != KDA_GATE_RAW && A_log) return KDA_ERR_SHAPE;
   return recurrent_impl(d, dt, q, k, v, gate, (int)gate_kind, A_log, qk_l2norm != 0, beta, h0, cu,
                         write_final, o, ht, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ scalar-gate delta rule
+namespace {
+
+kda_status gdn_gate_args(const kda_dims* d, kda_dtype dt, const kda_gdn_gate* g, kda::GdnGate* out) {
+  if (!g) return KDA_ERR_NULL;
+  if (!valid_dtype((kda_dtype)g->dtype) || (g->dtype == KDA_BF16 && dt != KDA_BF16)) return KDA_ERR_DTYPE;
+  if (g->kind != KDA_GATE_NAT && g->kind != KDA_GATE_RAW) return KDA_ERR_SHAPE;
+  if (g->kind != KDA_GATE_RAW && (g->A_log || g->dt_bias)) return KDA_ERR_SHAPE;
+  if ((size_t)d->B * d->T > 0 && !g->x) return KDA_ERR_NULL;
+  *out = kda::GdnGate{g->x, g->A_log, g->dt_bias, g->dtype == KDA_BF16, g->kind == KDA_GATE_RAW};
+  return KDA_OK;
+}
+
+bool gdn_chunk_supported(const kda_dims* d) {
+  return (d->K == 64 || d->K == 128) && (d->V == 64 || d->V == 128);
+}
+
+// Buffers of one call: every output is checked against every input and every
+// later output; pair (out, in) at equal addresses may be allowed.
+struct Buf {
+  const void* p;
+  size_t n;
+};
+kda_status check_alias(const Buf* outs, int no, const Buf* ins, int ni, const void* (*same)[2] = nullptr,
+                       int ns = 0) {
+  for (int i = 0; i < no; ++i) {
+    for (int j = 0; j < ni; ++j) {
+      if (!overlaps(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) continue;
+      bool ok = false;
+      for (int s = 0; s < ns; ++s)
+        ok |= outs[i].p == ins[j].p && outs[i].p == same[s][0] && ins[j].p == same[s][1];
+      if (!ok) return KDA_ERR_ALIAS;
+    }
+    for (int j = i + 1; j < no; ++j)
+      if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return KDA_ERR_ALIAS;
+  }
+  return KDA_OK;
+}
+
+// Checks shared by the forward entry points; sizes of the gate's buffers are
+// those of beta (per token and value head) and [HV].
+kda_status gdn_check_fwd(const kda_dims* d, kda_dtype dt, const void* q, const void* k, const void* v,
+                         const kda_gdn_gate* gate, const void* beta, const float* h0, const int32_t* cu,
+                         int32_t write_final, const void* o, const float* ht, const void* ws, size_t ws_n,
+                         kda::GdnGate* gg) {
+  kda_status st = check_dims(d, cu);
+  if (st != KDA_OK) return st;
+  if (!valid_dtype(dt)) return KDA_ERR_DTYPE;
+  st = gdn_gate_args(d, dt, gate, gg);
+  if (st != KDA_OK) return st;
+  if ((size_t)d->B * d->T > 0 && (!q || !k || !v || !beta || !o)) return KDA_ERR_NULL;
+  if (write_final && !ht && d->N > 0) return KDA_ERR_NULL;
+  const Sizes s = sizes(d, dt);
+  const size_t ge = esize((kda_dtype)gate->dtype), gx = (size_t)d->B * d->T * d->HV * ge;
+  const Buf outs[] = {{o, s.v}, {write_final ? ht : nullptr, s.state}, {ws, ws_n}};
+  const Buf ins[] = {{q, s.qk}, {k, s.qk}, {v, s.v}, {beta, s.beta}, {h0, s.state}, {gg->x, gx},
+                     {gg->A_log, d->HV * ge}, {gg->dt_bias, d->HV * ge},
+                     {cu, cu ? (size_t)(d->N + 1) * 4 : 0}};
+  const void* same[][2] = {{ht, h0}};
+  return check_alias(outs, 3, ins, 9, same, 1);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_gdn_chunk_workspace_bytes(const kda_dims* d, kda_dtype dt, int32_t backward) {
+  if (!d || !valid_dtype(dt) || !gdn_chunk_supported(d)) return 0;
+  if (d->N < 0 || d->T < 0 || d->B < 0 || d->HV <= 0 || d->H <= 0) return 0;
+  return kda_host::gdn_workspace_bytes(*d, dt, backward != 0);
+}
+
+kda_status kda_gdn_chunk_fwd(const kda_dims* d, kda_dtype dt, const void* q, const void* k, const void* v,
+                             const kda_gdn_gate* gate, int32_t l2, const void* beta, const float* h0,
+                             const int32_t* cu, int32_t write_final, void* o, float* ht, void* ws,
+                             size_t ws_bytes, hipStream_t stream) {
+  kda::GdnGate gg;
+  const size_t need = d ? kda_gdn_chunk_workspace_bytes(d, dt, 0) : 0;
+  kda_status st = gdn_check_fwd(d, dt, q, k, v, gate, beta, h0, cu, write_final, o, ht, ws, need, &gg);
+  if (st != KDA_OK) return st;
+  if (!gdn_chunk_supported(d)) return KDA_ERR_UNSUPPORTED;
+  if (d->N == 0) return KDA_OK;
+  if ((((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)o) & 15) || ((uintptr_t)ws & 255))
+    return KDA_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < need) return KDA_ERR_WORKSPACE;
+  return kda_host::launch_gdn_fwd(*d, dt, q, k, v, gg, l2 != 0, beta, h0, cu, write_final != 0, o, ht, ws,
+                                  stream) == hipSuccess
+             ? KDA_OK
+             : KDA_ERR_LAUNCH;
+}
+
+kda_status kda_gdn_chunk_bwd(const kda_dims* d, kda_dtype dt, const void* q, const void* k, const void* v,
+                             const kda_gdn_gate* gate, int32_t l2, const void* beta, const float* h0,
+                             const int32_t* cu, const void* do_, const float* dht, void* dq, void* dk,
+                             void* dv, void* dgate, void* dbeta, float* dh0, void* dA, void* ddt,
+                             void* ws, size_t ws_bytes, hipStream_t stream) {
+  kda_status st = check_dims(d, cu);
+  if (st != KDA_OK) return st;
+  if (!valid_dtype(dt)) return KDA_ERR_DTYPE;
+  kda::GdnGate gg;
+  st = gdn_gate_args(d, dt, gate, &gg);
+  if (st != KDA_OK) return st;
+  if ((gg.A_log == nullptr) != (dA == nullptr) || (gg.dt_bias == nullptr) != (ddt == nullptr))
+    return KDA_ERR_SHAPE;
+  if ((size_t)d->B * d->T > 0 &&
+      (!q || !k || !v || !beta || !do_ || !dq || !dk || !dv || !dgate || !dbeta))
+    return KDA_ERR_NULL;
+  if (!gdn_chunk_supported(d)) return KDA_ERR_UNSUPPORTED;
+  const size_t need = kda_gdn_chunk_workspace_bytes(d, dt, 1);
+  const Sizes s = sizes(d, dt);
+  const size_t ge = esize((kda_dtype)gate->dtype), gx = (size_t)d->B * d->T * d->HV * ge, gp = d->HV * ge;
+  const Buf outs[] = {{dq, s.qk}, {dk, s.qk}, {dv, s.v}, {dgate, gx}, {dbeta, s.beta}, {dh0, s.state},
+                      {dA, gp}, {ddt, gp}, {ws, need}};
+  const Buf ins[] = {{q, s.qk}, {k, s.qk}, {v, s.v}, {beta, s.beta}, {h0, s.state}, {gg.x, gx},
+                     {gg.A_log, gp}, {gg.dt_bias, gp}, {do_, s.v}, {dht, s.state},
+                     {cu, cu ? (size_t)(d->N + 1) * 4 : 0}};
+  st = check_alias(outs, 9, ins, 11);
+  if (st != KDA_OK) return st;
+  if ((((uintptr_t)q | (uintptr_t)k | (uintptr_t)v | (uintptr_t)do_ | (uintptr_t)dq | (uintptr_t)dk |
+        (uintptr_t)dv) & 15) || ((uintptr_t)ws & 255))
+    return KDA_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < need) return KDA_ERR_WORKSPACE;
+  if (d->N > 0 && kda_host::launch_gdn_refwd(*d, dt, q, k, v, gg, l2 != 0, beta, h0, cu, do_, dht, ws, stream) !=
+                      hipSuccess)
+    return KDA_ERR_LAUNCH;
+  return kda_host::launch_gdn_bwd(*d, dt, q, k, v, gg, l2 != 0, h0, cu, do_, dht, dq, dk, dv, dgate,
+                                  dbeta, dh0, dA, ddt, ws, stream) == hipSuccess
+             ? KDA_OK
+             : KDA_ERR_LAUNCH;
+}
+
+kda_status kda_gdn_recurrent_fwd(const kda_dims* d, kda_dtype dt, const void* q, const void* k, const void* v,
+                                 const kda_gdn_gate* gate, int32_t l2, const void* beta, const float* h0,
+                                 const int32_t* cu, int32_t write_final, void* o, float* ht,
+                                 hipStream_t stream) {
+  kda::GdnGate gg;
+  kda_status st = gdn_check_fwd(d, dt, q, k, v, gate, beta, h0, cu, write_final, o, ht, nullptr, 0, &gg);
+  if (st != KDA_OK) return st;
+  if (d->K > 256 || d->V > 256) return KDA_ERR_UNSUPPORTED;
+  return kda_host::launch_gdn_recurrent(*d, dt, q, k, v, gg, l2 != 0, beta, h0, cu, write_final != 0, o, ht,
+                                        stream) == hipSuccess
+             ? KDA_OK
+             : KDA_ERR_LAUNCH;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ output norm
+namespace {
+
+kda_status norm_check(kda_dtype dt, int64_t rows, const kda_norm* p, const int32_t* cu, int32_t N, int32_t rpt) {
+  if (!p) return KDA_ERR_NULL;
+  if (!valid_dtype(dt) || !valid_dtype((kda_dtype)p->param_dtype) ||
+      (p->param_dtype == KDA_BF16 && dt != KDA_BF16))
+    return KDA_ERR_DTYPE;
+  if (rows < 0 || p->D < 1 || !(p->eps >= 0.f) || p->eps > 3.0e38f) return KDA_ERR_SHAPE;
+  if (p->kind != KDA_NORM_RMS && p->kind != KDA_NORM_LAYER) return KDA_ERR_SHAPE;
+  if (p->activation != KDA_ACT_SILU && p->activation != KDA_ACT_SIGMOID) return KDA_ERR_SHAPE;
+  if (cu && (N < 0 || rpt < 1)) return KDA_ERR_SHAPE;
+  if (p->D > 8192) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_norm_fwd(kda_dtype dt, int64_t rows, const kda_norm* p, const int32_t* cu, int32_t N, int32_t rpt,
+                        const void* x, const void* gate, void* y, hipStream_t stream) {
+  kda_status st = norm_check(dt, rows, p, cu, N, rpt);
+  if (st != KDA_OK) return st;
+  if (rows == 0) return KDA_OK;
+  if (!x || !y) return KDA_ERR_NULL;
+  const size_t n = (size_t)rows * p->D * esize(dt), np = (size_t)p->D * esize((kda_dtype)p->param_dtype);
+  const Buf outs[] = {{y, n}};
+  const Buf ins[] = {{x, n}, {gate, gate ? n : 0}, {p->weight, np}, {p->bias, np},
+                     {cu, cu ? (size_t)(N + 1) * 4 : 0}};
+  const void* same[][2] = {{y, x}, {y, gate}};
+  st = check_alias(outs, 1, ins, 5, same, 2);
+  if (st != KDA_OK) return st;
+  return kda_host::launch_norm(dt, rows, *p, cu, N, rpt, x, gate, y, stream) == hipSuccess ? KDA_OK
+                                                                                           : KDA_ERR_LAUNCH;
+}
+
+size_t kda_norm_bwd_workspace_bytes(const kda_norm* p) {
+  if (!p || p->D < 1 || p->D > 8192) return 0;
+  return kda_host::norm_bwd_ws_bytes(p->D);
+}
+
+kda_status kda_norm_bwd(kda_dtype dt, int64_t rows, const kda_norm* p, const int32_t* cu, int32_t N, int32_t rpt,
+                        const void* x, const void* gate, const void* dy, void* dx, void* dgate, void* dw,
+                        void* db, void* ws, size_t ws_bytes, hipStream_t stream) {
+  kda_status st = norm_check(dt, rows, p, cu, N, rpt);
+  if (st != KDA_OK) return st;
+  // a gradient is produced exactly when its tensor is given
+  if ((p->weight == nullptr) != (dw == nullptr) || (p->bias == nullptr) != (db == nullptr)) return KDA_ERR_SHAPE;
+  if (rows > 0 && (gate == nullptr) != (dgate == nullptr)) return KDA_ERR_SHAPE;
+  if (rows > 0 && (!x || !dy || !dx)) return KDA_ERR_NULL;
+  const bool reduce = dw || db;
+  const size_t need = kda_norm_bwd_workspace_bytes(p);
+  if (reduce && (!ws || ws_bytes < need)) return KDA_ERR_WORKSPACE;
+  if (reduce && ((uintptr_t)ws & 15)) return KDA_ERR_UNSUPPORTED;
+  const size_t n = (size_t)rows * p->D * esize(dt), np = (size_t)p->D * esize((kda_dtype)p->param_dtype);
+  const Buf outs[] = {{dx, n}, {dgate, dgate ? n : 0}, {dw, np}, {db, np}, {reduce ? ws : nullptr, need}};
+  const Buf ins[] = {{x, n}, {gate, gate ? n : 0}, {dy, n}, {p->weight, np}, {p->bias, np},
+                     {cu, cu ? (size_t)(N + 1) * 4 : 0}};
+  const void* same[][2] = {{dx, x}, {dx, dy}, {dgate, gate}};
+  st = check_alias(outs, 5, ins, 6, same, 3);
+  if (st != KDA_OK) return st;
+  if (rows == 0 && !reduce) return KDA_OK;
+  return kda_host::launch_norm_bwd(dt, rows, *p, cu, N, rpt, x, gate, dy, dx, dgate, dw, db, ws, stream) ==
+                 hipSuccess
+             ? KDA_OK
+             : KDA_ERR_LAUNCH;
 }
 
 }  // extern "C"

@@ -1,0 +1,473 @@
+#pragma once
+// The gated delta rule with one decay per value head and token (scalar gate):
+// shared layouts and device helpers of its chunked kernels (gfx950).
+//
+// Per value head, with the FP32 state S [K, V] and natural-log gate g_t,
+//   S_t = e^{g_t} (I - b_t k_t k_t^T) S_{t-1} + b_t k_t v_t^T,  o_t = S_t^T q~_t,
+// q~ = q / sqrt(K). For a chunk of C = 64 tokens with start state S0, inclusive
+// gate sum G and e_ij = e^{G_i - G_j}:
+//   Abar_ij = (k_i . k_j) e_ij  (i > j),      P_ij = (q~_i . k_j) e_ij  (i >= j)
+//   M = (I + Abar diag(b))^-1 Abar            (strictly lower triangular)
+//   R = V - e^G K S0,   Y = R - M (b R),      Delta = b Y
+//   O = e^G (q~ S0) + P Delta,                S1 = e^{G_last} S0 + K^T (e^{G_last - G} Delta)
+// (Y = (I + Abar diag b)^-1 R written with M, so a zero b_t needs no division.)
+// Backward, from dS at the chunk's end:
+//   dDelta = P^T dO + e^{G_last - G} (K dS),  D = dDelta - M^T (b dDelta),  dV = E = b D
+//   dS0 = e^{G_last} dS + (e^G q~)^T dO - (e^G K)^T E
+// The gate's gradient (bf16 inputs; FP32's way is in kda_gdn_chunk_bwd.hip): scale
+// every state from token t on, and v_i and o_i for i >= t with it; nothing
+// changes but the decay into t. So dg_t = <S_T, dS_T> + sum_{i >= t} s_i over
+// the sequence's end T with s_i = <o_i, dO_i> - <v_i, dv_i>, two scalars per
+// token that the scans form in FP32. What a token adds to its own output is in
+// both and is left out of both, so that every term carries the decay (and a
+// strongly decaying head's small dg keeps its digits):
+//   s_i = <dO_i, o'_i - P_ii b_i (v_i - Y_i)> - b_i <v_i, D'_i>,
+//   o'_i = o_i - P_ii Delta_i,  D'_i = D_i - P_ii dO_i.
+// A decay that is one number per row and column never enters the products: k
+// and q go to the matrix cores as they are in memory (exact), the decays and
+// the optional L2 norms are row factors applied to the FP32 results. That is
+// what this form saves against a per-channel gate, whose decays have to be
+// multiplied into the operands.
+//
+// Rounding. q, k, v, dO enter exactly. In bf16, a computed operand x of a
+// product that feeds the state is carried as hi + lo, hi = bf16(x), lo =
+// bf16(x - hi): 2 (one split operand) or 3 (two) matrix-core steps leave a
+// relative error near 2^-17, so states and state gradients keep FP32 quality
+// through any number of chunks. What feeds only a bf16 output takes hi alone.
+#include "kda_chunk_kernels.h"
+
+namespace kda {
+
+// ------------------------------------------------------------------ index maps
+// Row r (0..15) of 16-row tile t stands for index 32 (t / 2) + 8 (r / 4) + 4 (t % 2)
+// + r % 4 (tokens and channels alike). An accumulator lane (column l16, rows
+// 4g .. 4g+3) of tiles 2s and 2s+1 then holds the eight consecutive indices
+// 32s + 8g .. +7 of its column, which is what the lane feeds as the operand of
+// the next product's contraction block s: results chain from product to
+// product in registers, and the other operand is one 16-byte read of eight
+// consecutive elements.
+__device__ __forceinline__ int perm_row(int t, int r) {
+  return 32 * (t >> 1) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);
+}
+// first of the four consecutive indices an accumulator lane holds
+__device__ __forceinline__ int perm_row4(int t, int g) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); }
+
+// Fragments of the 64 x 64 lower-triangular M and P (rows i, contraction over
+// j in blocks s of 32): tiles 0 and 1 need s = 0 only. Transposed (rows j,
+// contraction over i): tiles 2 and 3 need s = 1 only. Six of eight either way.
+__host__ __device__ constexpr int frag_low(int t, int s) { return t < 2 ? t : 2 * t - 2 + s; }
+__host__ __device__ constexpr int frag_up(int t, int s) { return t < 2 ? 2 * t + s : t + 2; }
+constexpr int kFragElems = 64 * 8;          // one fragment: [lane][8]
+constexpr int kTriElems = 6 * kFragElems;   // one triangular matrix
+
+// Row factors of a (chunk, value head), FP32 [kGdnScal][64] (one 16-byte aligned block):
+enum GdnScal : int {
+  kSk = 0,   // e^G rk                 (rk, rq: 1, or the inverse L2 norms of k and q rows)
+  kSq = 1,   // e^G rq / sqrt(K)
+  kSe = 2,   // e^{G_last - G} rk
+  kSb = 3,   // b
+  kSl = 4,   // [0] e^{G_last}
+  kSp = 5,   // backward only: P_ii
+  kSG = 6,   // backward only: G log2(e) as 64 doubles (two slots)
+  kSrq = 8,  // backward only: rq
+  kSrk = 9,  // backward only: rk
+  kGdnScal = 10
+};
+
+template <typename T>
+struct GdnWs {
+  static constexpr bool kScanGate = sizeof(T) == 2;  // dg from the scans' scalars
+  static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;  // hi + lo, or FP32
+  // forward: M (kParts), P; backward: M, P, M^T, P^T (kParts each), P without its diagonal
+  static constexpr size_t fwd = (size_t)kTriElems * (kParts + 1);
+  static constexpr size_t bwd = (size_t)kTriElems * (2 * kParts);  // one of its two pairs
+};
+
+// ------------------------------------------------------------------ operands
+// Eight consecutive contraction elements per lane: one bf16 fragment (one
+// 16x16x32 step), or eight FP32 values (eight 16x16x4 steps, lane group g
+// carrying element i of its eight in step i).
+template <typename T>
+struct Op8;
+template <>
+struct Op8<bf16> {
+  bf16x8 v;
+};
+template <>
+struct Op8<float> {
+  float v[8];
+};
+// a computed operand: hi + lo for bf16
+template <typename T>
+struct Op8s;
+template <>
+struct Op8s<bf16> {
+  bf16x8 hi, lo;
+};
+template <>
+struct Op8s<float> {
+  float v[8];
+};
+
+__device__ __forceinline__ f32x4 mma8(const Op8<bf16>& a, const Op8<bf16>& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma8(const Op8<float>& a, const Op8<float>& b, f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
+}
+// c + a b, b split
+__device__ __forceinline__ f32x4 mma8s(const Op8<bf16>& a, const Op8s<bf16>& b, f32x4 c) {
+  c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.lo, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.hi, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma8s(const Op8<float>& a, const Op8s<float>& b, f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
+  return c;
+}
+// c + a b with b's high part alone
+__device__ __forceinline__ f32x4 mma8h(const Op8<bf16>& a, const Op8s<bf16>& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.hi, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma8h(const Op8<float>& a, const Op8s<float>& b, f32x4 c) {
+  return mma8s(a, b, c);
+}
+
+// two accumulator tiles (2s, 2s + 1) as the operand of contraction block s
+__device__ __forceinline__ void make_op(Op8s<bf16>& o, const f32x4& t0, const f32x4& t1) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o.hi[e] = (bf16)t0[e];
+    o.hi[4 + e] = (bf16)t1[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o.lo[e] = (bf16)(t0[e] - (float)o.hi[e]);
+    o.lo[4 + e] = (bf16)(t1[e] - (float)o.hi[4 + e]);
+  }
+}
+__device__ __forceinline__ void make_op(Op8s<float>& o, const f32x4& t0, const f32x4& t1) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o.v[e] = t0[e];
+    o.v[4 + e] = t1[e];
+  }
+}
+__device__ __forceinline__ void make_op(Op8<bf16>& o, const f32x4& t0, const f32x4& t1) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o.v[e] = (bf16)t0[e];
+    o.v[4 + e] = (bf16)t1[e];
+  }
+}
+__device__ __forceinline__ void make_op(Op8<float>& o, const f32x4& t0, const f32x4& t1) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o.v[e] = t0[e];
+    o.v[4 + e] = t1[e];
+  }
+}
+
+// eight consecutive elements from 16-byte aligned memory
+__device__ __forceinline__ void ld_op(Op8<bf16>& o, const bf16* p) {
+  o.v = *reinterpret_cast<const bf16x8*>(p);
+}
+__device__ __forceinline__ void ld_op(Op8<float>& o, const float* p) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  o.v[0] = a.x; o.v[1] = a.y; o.v[2] = a.z; o.v[3] = a.w;
+  o.v[4] = b.x; o.v[5] = b.y; o.v[6] = b.z; o.v[7] = b.w;
+}
+__device__ __forceinline__ float op_get(const Op8<bf16>& o, int i) { return (float)o.v[i]; }
+__device__ __forceinline__ float op_get(const Op8<float>& o, int i) { return o.v[i]; }
+
+// ------------------------------------------------------------------ 4 x 4 transposes
+// Within each quad of lanes: lane a holds x[a][0..3] as four bf16 in two
+// registers; afterwards it holds x[0..3][a]. Its own inverse. It turns the
+// accumulator's four rows of one column into four columns of one row (one
+// 8-byte access in place of four 2-byte ones), and back.
+__device__ __forceinline__ uint2 quad_transpose(uint2 r) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t t0 = __builtin_amdgcn_update_dpp(0, (int)r.x, 0xB1, 0xF, 0xF, true);  // lane ^ 1
+  const uint32_t t1 = __builtin_amdgcn_update_dpp(0, (int)r.y, 0xB1, 0xF, 0xF, true);
+  const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
+  const uint32_t a0 = __builtin_amdgcn_perm(t0, r.x, sel), a1 = __builtin_amdgcn_perm(t1, r.y, sel);
+  const uint32_t u0 = __builtin_amdgcn_update_dpp(0, (int)a0, 0x4E, 0xF, 0xF, true);  // lane ^ 2
+  const uint32_t u1 = __builtin_amdgcn_update_dpp(0, (int)a1, 0x4E, 0xF, 0xF, true);
+  return (lane & 2) ? make_uint2(u1, a1) : make_uint2(a0, u0);
+}
+__device__ __forceinline__ uint2 pack4(const f32x4& x) {
+  const bf16x4 h = {(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
+  return __builtin_bit_cast(uint2, h);
+}
+__device__ __forceinline__ f32x4 unpack4(uint2 r) {
+  return f32x4{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u),
+               __uint_as_float(r.y << 16), __uint_as_float(r.y & 0xFFFF0000u)};
+}
+
+// A 16 x 16 tile between row-major memory and the accumulator layout. `row4`
+// is the lane's first row (perm_row4), rows row4 .. row4 + 3, column col0 + l16;
+// element (r, c) at p + r * stride + c, rows >= rows absent (zero / not
+// written). bf16: p 8-byte aligned, stride and col0 multiples of 4.
+template <typename T>
+struct TileRaw;
+template <>
+struct TileRaw<bf16> {
+  uint2 r;
+};
+template <>
+struct TileRaw<float> {
+  f32x4 r;
+};
+__device__ __forceinline__ void tile_ld(TileRaw<bf16>& t, const bf16* p, int64_t stride, int row4,
+                                        int col0, int rows) {
+  const int l16 = threadIdx.x & 15, row = row4 + (l16 & 3);
+  t.r = make_uint2(0, 0);
+  if (row < rows) t.r = *reinterpret_cast<const uint2*>(p + row * stride + col0 + 4 * (l16 >> 2));
+}
+__device__ __forceinline__ void tile_ld(TileRaw<float>& t, const float* p, int64_t stride, int row4,
+                                        int col0, int rows) {
+  const int l16 = threadIdx.x & 15;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) t.r[e] = row4 + e < rows ? p[(row4 + e) * stride + col0 + l16] : 0.f;
+}
+__device__ __forceinline__ f32x4 tile_get(const TileRaw<bf16>& t) { return unpack4(quad_transpose(t.r)); }
+__device__ __forceinline__ f32x4 tile_get(const TileRaw<float>& t) { return t.r; }
+// two tiles (2s, 2s + 1) straight as the operand of contraction block s
+__device__ __forceinline__ void tile_op(Op8<bf16>& o, const TileRaw<bf16>& t0, const TileRaw<bf16>& t1) {
+  const uint2 a = quad_transpose(t0.r), b = quad_transpose(t1.r);
+  o.v = __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
+}
+__device__ __forceinline__ void tile_op(Op8<float>& o, const TileRaw<float>& t0, const TileRaw<float>& t1) {
+  make_op(o, t0.r, t1.r);
+}
+__device__ __forceinline__ void tile_st(bf16* p, int64_t stride, int row4, int col0, int rows, const f32x4& x) {
+  const int l16 = threadIdx.x & 15, row = row4 + (l16 & 3);
+  const uint2 r = quad_transpose(pack4(x));
+  if (row < rows) *reinterpret_cast<uint2*>(p + row * stride + col0 + 4 * (l16 >> 2)) = r;
+}
+__device__ __forceinline__ void tile_st(float* p, int64_t stride, int row4, int col0, int rows, const f32x4& x) {
+  const int l16 = threadIdx.x & 15;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (row4 + e < rows) p[(row4 + e) * stride + col0 + l16] = x[e];
+}
+
+// sum over the 16 lanes that hold one accumulator row (rotations inside the
+// row: no LDS), in every lane
+template <int M>
+__device__ __forceinline__ float add_ror(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + M,
+                                                                   0xF, 0xF, false));
+}
+__device__ __forceinline__ float row16_sum(float x) {
+  return add_ror<8>(add_ror<4>(add_ror<2>(add_ror<1>(x))));
+}
+
+// ------------------------------------------------------------------ token tiles in LDS
+// A chunk's [64][K] rows of k or q, 16-byte blocks swizzled within each row:
+// block b of row r sits at b ^ swz(r). Both read patterns (16 rows of one
+// block column, as in a product over channels; four consecutive rows of four
+// blocks, as in a product over tokens) then spread over the banks.
+template <typename T, int K>
+struct TokTile {
+  static constexpr int kBlocks = K * (int)sizeof(T) / 16;  // 16-byte blocks per row
+  static constexpr size_t bytes = (size_t)kC * K * sizeof(T);
+  static constexpr int kUnits = kC * kBlocks;
+  static __device__ __forceinline__ int swz(int r) {
+    return kBlocks >= 16 ? ((r & 3) << 2) | ((r >> 3) & 3) : ((r & 3) << 1) | ((r >> 3) & 1);
+  }
+  static __device__ __forceinline__ int at(int r, int b) { return (r * kBlocks + (b ^ swz(r))) * 16; }
+  // rows perm_row(t, l16), channels 32 s + 8 g .. + 7
+  static __device__ __forceinline__ void rows(Op8<T>& o, const char* s, int t, int ks) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, r = perm_row(t, lane & 15);
+    if constexpr (sizeof(T) == 2) {
+      o.v = *reinterpret_cast<const bf16x8*>(s + at(r, 4 * ks + g));
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(s + at(r, 8 * ks + 2 * g));
+      const float4 b = *reinterpret_cast<const float4*>(s + at(r, 8 * ks + 2 * g + 1));
+      o.v[0] = a.x; o.v[1] = a.y; o.v[2] = a.z; o.v[3] = a.w;
+      o.v[4] = b.x; o.v[5] = b.y; o.v[6] = b.z; o.v[7] = b.w;
+    }
+  }
+  // channels perm_row(t, l16), tokens 32 s + 8 g .. + 7 (the transposed read:
+  // ds_read_b64_tr_b16 gives lane i of 16 column i of the four rows and four
+  // 8-byte blocks the 16 lanes point at)
+  static __device__ __forceinline__ void cols(Op8<T>& o, const char* s, int t, int ks) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+    if constexpr (sizeof(T) == 2) {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const int b = 4 * (t >> 1) + (l16 & 3), r0 = 32 * ks + 8 * g + (l16 >> 2);
+      const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)(s + at(r0, b) + 8 * (t & 1)));
+      const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)(s + at(r0 + 4, b) + 8 * (t & 1)));
+      const uint2 a = __builtin_bit_cast(uint2, x0), c = __builtin_bit_cast(uint2, x1);
+      o.v = __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, c.x, c.y));
+    } else {
+      const int c = perm_row(t, l16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = 32 * ks + 8 * g + i;
+        o.v[i] = *reinterpret_cast<const float*>(s + at(r, c >> 2) + 4 * (c & 3));
+      }
+    }
+  }
+  // accumulator-layout tile: rows perm_row4(tt, g) + e, channel perm_row(ct, l16)
+  static __device__ __forceinline__ f32x4 tile(const char* s, int tt, int ct) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+    if constexpr (sizeof(T) == 2) {
+      const int r = perm_row4(tt, g) + (l16 & 3), b = 4 * (ct >> 1) + (l16 >> 2);
+      const uint2 x = *reinterpret_cast<const uint2*>(s + at(r, b) + 8 * (ct & 1));
+      return unpack4(quad_transpose(x));
+    } else {
+      const int c = perm_row(ct, l16);
+      f32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = *reinterpret_cast<const float*>(s + at(perm_row4(tt, g) + e, c >> 2) + 4 * (c & 3));
+      return x;
+    }
+  }
+};
+
+// ------------------------------------------------------------------ global memory -> LDS
+// One wave's 1 KB: lane i's 16 bytes at `src` go to dst + 16 i (dst uniform in
+// the wave) without passing through registers. Complete after lds_dma_wait().
+__device__ __forceinline__ void lds_dma(const void* src, char* dst) {
+  typedef __attribute__((address_space(1))) const void gvoid;
+  typedef __attribute__((address_space(3))) void lvoid;
+  __builtin_amdgcn_global_load_lds((gvoid*)src, (lvoid*)dst, 16, 0, 0);
+}
+__device__ __forceinline__ void lds_dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// token tile of chunk rows p + r * stride (elements), r < L; rows past L repeat
+// row L - 1 (their factors are zero)
+template <typename T, int K, int NW>
+__device__ __forceinline__ void dma_tok_tile(char* dst, const T* p, int64_t stride, int L, int wave) {
+  using TT = TokTile<T, K>;
+  static_assert(TT::kUnits % (64 * NW) == 0, "whole waves");
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int n = 0; n < TT::kUnits / (64 * NW); ++n) {
+    const int i = n * NW + wave;
+    const int u = 64 * i + lane, r = u / TT::kBlocks, b = (u % TT::kBlocks) ^ TT::swz(r);
+    lds_dma(reinterpret_cast<const char*>(p + min(r, L - 1) * stride) + 16 * b, dst + 1024 * i);
+  }
+}
+// `bytes` (a multiple of 1 KB) of contiguous memory
+template <int BYTES, int NW>
+__device__ __forceinline__ void dma_flat(char* dst, const void* src, int wave) {
+  static_assert(BYTES % 1024 == 0, "whole waves");
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int n = 0; n < (BYTES / 1024 + NW - 1) / NW; ++n) {
+    const int i = n * NW + wave;
+    if (i >= BYTES / 1024) break;
+    lds_dma(reinterpret_cast<const char*>(src) + 1024 * i + 16 * lane, dst + 1024 * i);
+  }
+}
+
+// ------------------------------------------------------------------ gate
+struct GdnGate {
+  const void* x;        // [B, T, HV]
+  const void* A_log;    // [HV] or null
+  const void* dt_bias;  // [HV] or null
+  int bf;               // all three are bf16 (else FP32)
+  int raw;              // x is the raw input (else the natural-log gate)
+};
+__device__ __forceinline__ float ld_any(const void* p, int64_t i, int bf) {
+  return bf ? (float)reinterpret_cast<const bf16*>(p)[i] : reinterpret_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void st_any(void* p, int64_t i, int bf, float x) {
+  if (bf) reinterpret_cast<bf16*>(p)[i] = (bf16)x;
+  else reinterpret_cast<float*>(p)[i] = x;
+}
+// natural-log gate of flat entry i (head hv); pre-activation in *xb
+__device__ __forceinline__ float gdn_gate(const GdnGate& g, int64_t i, int hv, float* xb, float* scale) {
+  const float x = ld_any(g.x, i, g.bf);
+  if (!g.raw) {
+    *xb = x;
+    *scale = 1.f;
+    return x;
+  }
+  const float a = g.A_log ? expf(ld_any(g.A_log, hv, g.bf)) : 1.f;
+  const float y = g.dt_bias ? x + ld_any(g.dt_bias, hv, g.bf) : x;
+  *xb = y;
+  *scale = a;
+  return -a * softplus_f32(y);
+}
+
+}  // namespace kda
+
+namespace kda_host {
+size_t gdn_workspace_bytes(const kda_dims& d, kda_dtype dt, int bwd);
+hipError_t launch_gdn_fwd(const kda_dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
+                          const kda::GdnGate& gate, int l2, const void* beta, const float* h0,
+                          const int32_t* cu, int write_final, void* o, float* ht, void* ws,
+                          hipStream_t s);
+// the backward's own run over the forward: fragments, states, Y and <o, dO>
+hipError_t launch_gdn_refwd(const kda_dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
+                            const kda::GdnGate& gate, int l2, const void* beta, const float* h0,
+                            const int32_t* cu, const void* dO, const float* dht, void* ws,
+                            hipStream_t s);
+hipError_t launch_gdn_bwd(const kda_dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
+                          const kda::GdnGate& gate, int l2, const float* h0, const int32_t* cu,
+                          const void* dO, const float* dht, void* dq, void* dk, void* dv, void* dgate,
+                          void* dbeta, float* dh0, void* dA_log, void* d_dt_bias, void* ws,
+                          hipStream_t s);
+hipError_t launch_gdn_recurrent(const kda_dims& d, kda_dtype dt, const void* q, const void* k,
+                                const void* v, const kda::GdnGate& gate, int l2, const void* beta,
+                                const float* h0, const int32_t* cu, int write_final, void* o,
+                                float* ht, hipStream_t s);
+}  // namespace kda_host
+
+namespace kda {
+// Workspace of a chunked call, in order: the varlen chunk table, then per
+// (chunk, value head): row factors and fragments, and for the backward S0, Y,
+// dS, D, the per-token scalars of each 16 columns and the gate-parameter partials.
+template <typename T>
+struct GdnLayout {
+  int* table;
+  float* scal;   // [chunk * HV + hv][kGdnScal][64]
+  T* frag;       // [..][GdnWs<T>::fwd], or for the backward [..][GdnWs<T>::bwd]: M, P
+  T* fragT;      // [..][GdnWs<T>::bwd]: M^T, P^T
+  T* S0;         // [..][K][V]
+  T* Y;          // [..][64][V]
+  T* dS;         // [..][K][V]
+  T* D;          // [..][64][V]
+  float* tok;    // [..][V / 16][64]: <o, dO> of the columns, then their share of dg
+  float* end;    // [N * HV][V / 16]: <S_T, dS_T> of the columns
+  float* par;    // [..][2]
+  size_t bytes;
+  GdnLayout(const kda_dims& d, bool varlen, void* ws, bool bwd) {
+    const int64_t mc = max_chunks(d, varlen);
+    const size_t n = (size_t)mc * d.HV;
+    char* p = reinterpret_cast<char*>(ws);
+    auto take = [&](size_t b) {
+      char* r = p;
+      p += align256(b);
+      return r;
+    };
+    char* p0 = p;
+    table = reinterpret_cast<int*>(take(sizeof(int) * (size_t)(2 + 2 * (size_t)d.N + mc)));
+    scal = reinterpret_cast<float*>(take(n * kGdnScal * kC * sizeof(float)));
+    frag = reinterpret_cast<T*>(take(n * (bwd ? GdnWs<T>::bwd : GdnWs<T>::fwd) * sizeof(T)));
+    fragT = S0 = Y = dS = D = nullptr;
+    tok = end = par = nullptr;
+    if (bwd) {
+      fragT = reinterpret_cast<T*>(take(n * GdnWs<T>::bwd * sizeof(T)));
+      S0 = reinterpret_cast<T*>(take(n * d.K * d.V * sizeof(T)));
+      Y = reinterpret_cast<T*>(take(n * kC * d.V * sizeof(T)));
+      dS = reinterpret_cast<T*>(take(n * d.K * d.V * sizeof(T)));
+      D = reinterpret_cast<T*>(take(n * kC * d.V * sizeof(T)));
+      tok = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
+      end = reinterpret_cast<float*>(take((size_t)d.N * d.HV * (d.V / 16) * sizeof(float)));
+      par = reinterpret_cast<float*>(take(n * 2 * sizeof(float)));
+    }
+    bytes = (size_t)(p - p0);
+  }
+};
+}  // namespace kda

@@ -1,0 +1,740 @@
+// Chunked gated delta rule with a scalar gate, backward. Formulas, layouts and
+// the rounding rule are in kda_gdn.h.
+//
+//   gdn_rev_scan_kernel   one wave per 16 columns of one (sequence, value head)
+//                         state gradient, walking the chunks backwards; writes
+//                         dv, the columns' share of dg, and per chunk dS (at the
+//                         chunk's end) and D.
+//   gdn_local_kernel      one workgroup per (chunk, q/k head), wave w owning
+//                         token tile w: dq, dk (summed over the head's value
+//                         heads) and dbeta from the chunk's S0, Y, dS and D, and
+//                         the gate's gradient from the shares of dg.
+//   gdn_par_kernel        dA_log and d_dt_bias from per-chunk partial sums.
+//
+// With dP = dO Delta^T and dE = E Delta^T (64 x 64) the gradients of k, q are
+//   dq~ = e^G (dO S0^T) + (e . dP) K                          (lower triangle)
+//   dk  = e^{G_last - G} (Delta dS^T) - e^G (E S0^T)
+//         + (e . dP)^T q~ - (e . dE) K - (e . dE)^T K         (dE strictly lower)
+// S0, Y, dS and D pass between the kernels rounded to the inputs' type: they
+// feed dq, dk and dbeta, which are rounded to it as well.
+//
+// The gate's gradient comes one of two ways.
+//   bf16: dg_t = <S_T, dS_T> + sum_{i >= t} s_i over the sequence (kda_gdn.h), from
+//     FP32 values inside the scans, summed in double. Formed from the rounded S0, Y, dS and D instead it was off by 2e-3, and
+//     dA_log and d_dt_bias, which sum it over tokens of either sign, by 1e-2
+//     and more. What is left (1e-6 of a token's two scalars, adding up like a
+//     random walk over the sequence) is far below bf16.
+//   FP32: the operands are exact, the walk would not be small enough, and dg is
+//     taken chunk by chunk: what the decay between tokens t - 1 and t scales is
+//     the rows i >= t against S0, the columns j < t towards the chunk's end and
+//     the pairs i >= t > j,
+//       dg_t = e^{G_last} <S0, dS> + sum_{j < t} c_j + sum_{i >= t} (r_i + sum_{j < i} X_ij - sum_{n > i} X_ni),
+//       c_j = <k_j, e^{G_last - G_j} dS Delta_j>,  r_i = <q~_i, e^G S0 dO_i> - <k_i, e^G S0 E_i>,
+//       X_ij = e_ij (dP_ij q~_i.k_j - dE_ij k_i.k_j)                          (i > j);
+//     pairs on one side of t cancel exactly, as both sums add the same X_ij.
+#include "kda_gdn.h"
+
+namespace kda {
+
+// ------------------------------------------------------------------ reverse scan
+template <typename T, int K>
+struct GdnRevLds {
+  static constexpr size_t tok = TokTile<T, K>::bytes;
+  static constexpr size_t tri = GdnWs<T>::bwd * sizeof(T);  // M^T, P^T (all parts)
+  static constexpr size_t oQ = tok;
+  static constexpr size_t oM = 2 * tok;
+  static constexpr size_t oS = oM + tri;
+  static constexpr int scal = 8 * kC * (int)sizeof(float);  // row factors 0..7
+  static constexpr size_t buf = oS + scal;
+  static constexpr int nbuf = sizeof(T) == 2 ? 2 : 1;
+  static constexpr size_t total = nbuf * buf;
+};
+
+template <typename T, int K, int V, int NW>
+__global__ void __launch_bounds__(NW * 64)
+gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                    const T* __restrict__ dO, const float* __restrict__ dht, const int32_t* __restrict__ cu,
+                    const int* __restrict__ table, int N, int T_, int H, int HV,
+                    const float* __restrict__ ws_scal, const T* __restrict__ ws_bwd,
+                    T* __restrict__ dv, float* __restrict__ dh0, T* __restrict__ ws_dS,
+                    T* __restrict__ ws_D, float* __restrict__ ws_tok, const float* __restrict__ ws_end) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  __shared__ __attribute__((aligned(16))) float s_tok[NW][kC];
+  using Lds = GdnRevLds<T, K>;
+  using TT = TokTile<T, K>;
+  constexpr int NK = K / 32, RT = K / 16, BV = 16 * NW, NVB = V / BV, PT = GdnWs<T>::kParts;
+  constexpr bool kGate = GdnWs<T>::kScanGate;
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = blockIdx.x / (8 * NVB), in = blockIdx.x % (8 * NVB);
+  const int64_t chain = (int64_t)grp * 8 + in % 8;
+  if (chain >= (int64_t)N * HV) return;
+  const int n = cu ? table[2 + N + (int)(chain / HV)] : (int)(chain / HV);
+  const int hv = (int)(chain % HV), h = hv / (HV / H);
+  const int col0 = (in / 8) * BV + 16 * wave;
+  int64_t bos;
+  int len;
+  seq_range(cu, n, T_, &bos, &len);
+  const size_t st = ((size_t)n * HV + hv) * (size_t)K * V;
+  if (len <= 0) {
+    if (!dh0) return;
+    for (int e = lane; e < K * 16; e += 64) {
+      const size_t off = st + (size_t)(e >> 4) * V + col0 + (e & 15);
+      dh0[off] = dht ? dht[off] : 0.f;
+    }
+    return;
+  }
+  const int nc = (len + kC - 1) / kC;
+  const int64_t c0 = cu ? table[1 + n] : (int64_t)n * ((T_ + kC - 1) / kC);
+
+  auto fetch = [&](int c, char* b) {
+    const size_t ch = (size_t)(c0 + c) * HV + hv;
+    const int64_t row = ((bos + (int64_t)c * kC) * H + h) * K;
+    const int L = min(kC, len - c * kC);
+    dma_tok_tile<T, K, NW>(b, k + row, (int64_t)H * K, L, wave);
+    dma_tok_tile<T, K, NW>(b + Lds::oQ, q + row, (int64_t)H * K, L, wave);
+    dma_flat<(int)Lds::tri, NW>(b + Lds::oM, ws_bwd + ch * GdnWs<T>::bwd, wave);
+    dma_flat<Lds::scal, NW>(b + Lds::oS, ws_scal + ch * (kGdnScal * kC), wave);
+  };
+  TileRaw<T> dr[4], vr[4];
+  float gl, od;
+  auto fetch_do = [&](int c) {
+    const int L = min(kC, len - c * kC);
+    const int64_t at = ((bos + (int64_t)c * kC) * HV + hv) * V;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      tile_ld(dr[t], dO + at, (int64_t)HV * V, perm_row4(t, g), col0, L);
+      if constexpr (kGate) tile_ld(vr[t], v + at, (int64_t)HV * V, perm_row4(t, g), col0, L);
+    }
+    if constexpr (kGate) od = ws_tok[(((size_t)(c0 + c) * HV + hv) * (V / 16) + (col0 >> 4)) * kC + lane];
+    gl = ws_scal[((size_t)(c0 + c) * HV + hv) * (kGdnScal * kC) + kSl * kC];
+  };
+
+  f32x4 S[RT];  // dS
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      S[r][e] = dht ? dht[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] : 0.f;
+
+  // sum over the tokens behind this chunk of <o, dO> - <v, dv>, these columns
+  double behind = kGate && dht ? (double)ws_end[((size_t)n * HV + hv) * (V / 16) + (col0 >> 4)] : 0.;
+  int buf = 0;
+  fetch(nc - 1, smem);
+  fetch_do(nc - 1);
+  for (int c = nc - 1; c >= 0; --c) {
+    const char* b = smem + buf * Lds::buf;
+    lds_dma_wait();
+    __syncthreads();
+    if (Lds::nbuf == 2) {
+      buf ^= 1;
+      if (c > 0) fetch(c - 1, smem + buf * Lds::buf);
+    }
+    const float* sf = reinterpret_cast<const float*>(b + Lds::oS);
+    const T* sM = reinterpret_cast<const T*>(b + Lds::oM);
+    const T* sP = sM + PT * kTriElems;
+    const size_t ch = (size_t)(c0 + c) * HV + hv;
+    const int L = min(kC, len - c * kC);
+    f32x4 dot[4];
+    Op8<T> dop[2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) dot[t] = tile_get(dr[t]);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) tile_op(dop[s], dr[2 * s], dr[2 * s + 1]);
+    f32x4 vt[4];
+    if constexpr (kGate) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) vt[t] = tile_get(vr[t]);
+    }
+    const float el = gl, od_c = kGate ? od : 0.f;
+    if (c > 0) fetch_do(c - 1);
+
+#pragma unroll
+    for (int r = 0; r < RT; ++r) tile_st(ws_dS + ch * K * V, V, perm_row4(r, g), col0, K, S[r]);
+    // dDelta = P^T dO + e^{G_last - G} (k dS), P's diagonal apart
+    f32x4 x[4], p[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) x[t] = p[t] = zero4();
+#pragma unroll
+    for (int s = 0; s < NK; ++s) {
+      Op8s<T> sb;
+      make_op(sb, S[2 * s], S[2 * s + 1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        Op8<T> a;
+        TT::rows(a, b, t, s);
+        x[t] = mma8s(a, sb, x[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int s = (t >> 1); s < 2; ++s) {
+        Op8<T> a;
+#pragma unroll
+        for (int pt = PT - 1; pt >= 0; --pt) {
+          ld_op(a, sP + pt * kTriElems + frag_up(t, s) * kFragElems + lane * 8);
+          p[t] = mma8(a, dop[s], p[t]);
+        }
+      }
+    f32x4 bb[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float f[4], w[4], pd[4];
+      lds4(sf + kSe * kC + perm_row4(t, g), f);
+      lds4(sf + kSb * kC + perm_row4(t, g), w);
+      lds4(sf + kSp * kC + perm_row4(t, g), pd);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[t][e] = fmaf(f[e], x[t][e], p[t][e]);
+        p[t][e] = pd[e] * dot[t][e];
+        bb[t][e] = w[e];
+      }
+    }
+    // D' = dDelta' - M^T (b dDelta), D = D' + P_ii dO
+    {
+      Op8s<T> rb[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        f32x4 a0, a1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a0[e] = -bb[2 * s][e] * (x[2 * s][e] + p[2 * s][e]);
+          a1[e] = -bb[2 * s + 1][e] * (x[2 * s + 1][e] + p[2 * s + 1][e]);
+        }
+        make_op(rb[s], a0, a1);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int s = (t >> 1); s < 2; ++s) {
+          Op8<T> a;
+          if constexpr (sizeof(T) == 2) {
+            ld_op(a, sM + kTriElems + frag_up(t, s) * kFragElems + lane * 8);
+            x[t] = mma8h(a, rb[s], x[t]);
+          }
+          ld_op(a, sM + frag_up(t, s) * kFragElems + lane * 8);
+          x[t] = mma8s(a, rb[s], x[t]);
+        }
+    }
+    if constexpr (kGate) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = row16_sum(bb[t][e] * x[t][e] * vt[t][e]);
+        if (l16 == 0)
+          *reinterpret_cast<float4*>(&s_tok[wave][perm_row4(t, g)]) = make_float4(y[0], y[1], y[2], y[3]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[t][e] += p[t][e];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) tile_st(ws_D + ch * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+    // dv = E = b D; dS0 = e^{G_last} dS + q^T (e^G rq/sqrt(K) dO) - k^T (e^G rk E)
+    Op8s<T> qb[2], kb[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      f32x4 eq[2], ek[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 2 * s + i;
+        float fq[4], fk[4];
+        lds4(sf + kSq * kC + perm_row4(t, g), fq);
+        lds4(sf + kSk * kC + perm_row4(t, g), fk);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[t][e] *= bb[t][e];
+          eq[i][e] = fq[e] * dot[t][e];
+          ek[i][e] = -fk[e] * x[t][e];
+        }
+      }
+      make_op(qb[s], eq[0], eq[1]);
+      make_op(kb[s], ek[0], ek[1]);
+    }
+    T* vb = dv + ((bos + (int64_t)c * kC) * HV + hv) * V;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      tile_st(vb, (int64_t)HV * V, perm_row4(t, g), col0, L, x[t]);
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[r][e] *= el;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Op8<T> a;
+        TT::cols(a, b + Lds::oQ, r, s);
+        S[r] = mma8s(a, qb[s], S[r]);
+        TT::cols(a, b, r, s);
+        S[r] = mma8s(a, kb[s], S[r]);
+      }
+    }
+    // the columns' share of dg: lane = token, sums from the sequence's end
+    if constexpr (kGate) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      double y = lane < L ? (double)od_c - (double)s_tok[wave][lane] : 0.;
+#pragma unroll
+      for (int i = 1; i < 64; i <<= 1) {
+        const double z = __shfl_down(y, i);
+        if (lane + i < 64) y += z;
+      }
+      y += behind;
+      behind = __shfl(y, 0);
+      ws_tok[(ch * (V / 16) + (col0 >> 4)) * kC + lane] = (float)y;
+    }
+    if (Lds::nbuf == 1 && c > 0) {
+      __syncthreads();
+      fetch(c - 1, smem);
+    }
+  }
+  if (dh0) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        dh0[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] = S[r][e];
+  }
+}
+
+// ------------------------------------------------------------------ local gradients
+template <typename T>
+__device__ __forceinline__ float op_dot(const Op8<T>& a, const Op8<T>& b) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(op_get(a, i), op_get(b, i), s);
+  return s;
+}
+
+template <typename T, int K, int V>
+__global__ void __launch_bounds__(256)
+gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ dO, GdnGate gate,
+                 const int32_t* __restrict__ cu, const int* __restrict__ table, int N, int T_, int H,
+                 int HV, int l2, int has_h0, float scale, const float* __restrict__ ws_scal,
+                 const T* __restrict__ ws_S0, const T* __restrict__ ws_Y, const T* __restrict__ ws_dS,
+                 const T* __restrict__ ws_D, const float* __restrict__ ws_tok, T* __restrict__ dq, T* __restrict__ dk,
+                 T* __restrict__ dbeta, void* __restrict__ dgate, float* __restrict__ par) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  using TT = TokTile<T, K>;
+  constexpr int NV = V / 32, RT = K / 16;
+  __shared__ double sG[kC];
+  constexpr bool kDirect = !GdnWs<T>::kScanGate;
+  __shared__ __attribute__((aligned(16))) float sB[kC];
+  __shared__ __attribute__((aligned(16))) float sR[kDirect ? kC : 4], sC[kDirect ? kC : 4];
+  __shared__ float sS[4], sX[kDirect ? kC : 1], sXc[4][kDirect ? kC : 1];
+  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int j = blockIdx.x / H, h = blockIdx.x % H, grp = HV / H;
+  const ChunkGeo geo = chunk_geo(j, cu, table, N, T_);
+  if (!geo.ok) return;
+  const int L = geo.L;
+  char* sK = smem;
+  char* sQ = smem + TT::bytes;
+  {
+    const int64_t row = (geo.t0 * H + h) * K;
+    dma_tok_tile<T, K, 4>(sK, k + row, (int64_t)H * K, L, wave);
+    dma_tok_tile<T, K, 4>(sQ, q + row, (int64_t)H * K, L, wave);
+  }
+  const int own = perm_row(wave, l16);   // this lane's row as an operand
+  const int own4 = perm_row4(wave, g);   // first of its four accumulator rows
+  const int p = wave >> 1;               // 32-token block of the wave's tokens
+  f32x4 aq[RT], ak[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) aq[r] = ak[r] = zero4();
+  f32x4 rq4, rk4;  // q and k norms of the lane's rows (scale included in neither)
+
+  for (int hh = 0; hh < grp; ++hh) {
+    const int hv = h * grp + hh;
+    const size_t ch = (size_t)j * HV + hv;
+    const float* sc = ws_scal + ch * (kGdnScal * kC);
+    if (tid < kC) {
+      sG[tid] = reinterpret_cast<const double*>(sc + kSG * kC)[tid];
+      sB[tid] = sc[kSb * kC + tid];
+    }
+    // operands of the wave's own rows
+    Op8<T> od[NV], oD[NV], oY[NV];
+    const T* dOb = dO + (geo.t0 * HV + hv) * V;
+    const T* Db = ws_D + ch * kC * V;
+    const T* Yb = ws_Y + ch * kC * V;
+#pragma unroll
+    for (int s = 0; s < NV; ++s) {
+      ld_op(od[s], dOb + (int64_t)min(own, L - 1) * HV * V + 32 * s + 8 * g);
+      ld_op(oD[s], Db + own * V + 32 * s + 8 * g);
+      ld_op(oY[s], Yb + own * V + 32 * s + 8 * g);
+    }
+    float fk[4], fq[4], fe[4], fb[4], frq[4], frk[4];
+    lds4(sc + kSk * kC + own4, fk);
+    lds4(sc + kSq * kC + own4, fq);
+    lds4(sc + kSe * kC + own4, fe);
+    lds4(sc + kSb * kC + own4, fb);
+    lds4(sc + kSrq * kC + own4, frq);
+    lds4(sc + kSrk * kC + own4, frk);
+    if (hh == 0) lds_dma_wait();
+    __syncthreads();  // gate sums and b (and the token tiles) are in LDS
+
+    // dbeta_i = <D_i, Y_i>
+    {
+      float x = 0.f;
+#pragma unroll
+      for (int s = 0; s < NV; ++s) x += op_dot(oD[s], oY[s]);
+      x += __shfl_xor(x, 16);
+      x += __shfl_xor(x, 32);
+      if (g == 0 && own < L) dbeta[(geo.t0 + own) * HV + hv] = from_f32<T>(x);
+    }
+    // 64 x 64 parts. As rows (contraction over j): W_ij = e_ij b_j rk_j / sqrt(K) dO_i.Y_j and
+    // Z_ij = - e_ij b_i b_j rk_j D_i.Y_j, from the products with Y's rows on the left, so the
+    // accumulators are the operand with the wave's tokens as rows. As columns (contraction
+    // over i): W'_ij = e_ij b_j rq_i / sqrt(K) dO_i.Y_j, Z'_ij = - e_ij b_i b_j rk_i D_i.Y_j.
+    Op8<T> wr[2], zr[2], wc[2], zc[2];
+    const double Go = sG[own];
+    const float bo = sB[own], rqo = sc[kSrq * kC + own], rko = sc[kSrk * kC + own];
+    float xrow = 0.f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      f32x4 w[2], z[2], w2[2], z2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[i] = z[i] = w2[i] = z2[i] = zero4();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int row = perm_row(2 * s + i, l16), row4 = perm_row4(2 * s + i, g);
+        f32x4 qk = zero4(), kk = zero4();
+        if constexpr (kDirect) {
+          if (s <= p) {
+#pragma unroll
+            for (int u = 0; u < K / 32; ++u) {
+              Op8<T> kj, qi, ki;
+              TT::rows(kj, sK, 2 * s + i, u);
+              TT::rows(qi, sQ, wave, u);
+              TT::rows(ki, sK, wave, u);
+              qk = mma8(kj, qi, qk);
+              kk = mma8(kj, ki, kk);
+            }
+          }
+        }
+        if (s <= p) {
+#pragma unroll
+          for (int u = 0; u < NV; ++u) {
+            Op8<T> y;
+            ld_op(y, Yb + row * V + 32 * u + 8 * g);
+            w[i] = mma8(y, od[u], w[i]);
+            z[i] = mma8(y, oD[u], z[i]);
+          }
+        }
+        if (s >= p) {
+#pragma unroll
+          for (int u = 0; u < NV; ++u) {
+            Op8<T> a, d;
+            ld_op(a, dOb + (int64_t)min(row, L - 1) * HV * V + 32 * u + 8 * g);
+            ld_op(d, Db + row * V + 32 * u + 8 * g);
+            w2[i] = mma8(a, oY[u], w2[i]);
+            z2[i] = mma8(d, oY[u], z2[i]);
+          }
+        }
+        float b4[4], rq_[4], rk_[4];
+        lds4(sB + row4, b4);
+        lds4(sc + kSrq * kC + row4, rq_);
+        lds4(sc + kSrk * kC + row4, rk_);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int o = row4 + e;  // the other token: j of w, z; i of w2, z2
+          const double d = Go - sG[o];
+          const float ej = own >= o && own < L ? ex2((float)d) * b4[e] * rk_[e] : 0.f;
+          const float ei = o >= own && o < L ? ex2((float)-d) * bo : 0.f;
+          w[i][e] *= ej * scale;
+          z[i][e] = own > o ? -z[i][e] * ej * bo : 0.f;
+          w2[i][e] *= ei * rq_[e] * scale;
+          z2[i][e] = o > own ? -z2[i][e] * ei * b4[e] * rk_[e] : 0.f;
+          if constexpr (kDirect) {
+            const float x = own > o ? w[i][e] * rqo * qk[e] + z[i][e] * rko * kk[e] : 0.f;
+            xrow += x;
+            const float xc = row16_sum(x);
+            if (l16 == 0) sXc[wave][o] = xc;
+          }
+        }
+      }
+      make_op(wr[s], w[0], w[1]);
+      make_op(zr[s], z[0], z[1]);
+      make_op(wc[s], w2[0], w2[1]);
+      make_op(zc[s], z2[0], z2[1]);
+    }
+    if constexpr (kDirect) {
+      xrow += __shfl_xor(xrow, 16);
+      xrow += __shfl_xor(xrow, 32);
+      if (g == 0) sX[own] = xrow;
+    }
+    // channel tiles
+    float rr[4] = {0.f, 0.f, 0.f, 0.f}, cc[4] = {0.f, 0.f, 0.f, 0.f}, sds = 0.f;
+    const T* S0b = ws_S0 + ch * K * V;
+    const T* dSb = ws_dS + ch * K * V;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int c = perm_row(r, l16);
+      f32x4 a1 = zero4(), a2 = zero4(), a3 = zero4();
+#pragma unroll
+      for (int s = 0; s < NV; ++s) {
+        Op8<T> s0, ds;
+        ld_op(s0, S0b + (size_t)c * V + 32 * s + 8 * g);
+        ld_op(ds, dSb + (size_t)c * V + 32 * s + 8 * g);
+        a1 = mma8(od[s], s0, a1);
+        a2 = mma8(oD[s], s0, a2);
+        a3 = mma8(oY[s], ds, a3);
+        if constexpr (kDirect) {
+          if ((r & 3) == wave) sds += op_dot(s0, ds);
+        }
+      }
+      f32x4 tq = zero4(), tr = zero4(), tc = zero4();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Op8<T> kc, qc;
+        TT::cols(kc, sK, r, s);
+        TT::cols(qc, sQ, r, s);
+        if (s <= p) {
+          tq = mma8(wr[s], kc, tq);
+          tr = mma8(zr[s], kc, tr);
+        }
+        if (s >= p) {
+          tc = mma8(wc[s], qc, tc);
+          tc = mma8(zc[s], kc, tc);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // fq = e^G rq / sqrt(K), fk = e^G rk, fe = e^{G_last - G} rk: gradients of the
+        // normalised rows, times their own inverse norm
+        aq[r][e] += a1[e] * fq[e] + frq[e] * tq[e];
+        ak[r][e] += (a3[e] * fe[e] - a2[e] * fk[e]) * fb[e] + frk[e] * (tr[e] + tc[e]);
+      }
+      if constexpr (kDirect) {
+        const f32x4 qt = TT::tile(sQ, wave, r), kt = TT::tile(sK, wave, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          rr[e] += qt[e] * a1[e] * fq[e] - kt[e] * a2[e] * fk[e] * fb[e];
+          cc[e] += kt[e] * a3[e] * fe[e] * fb[e];
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one tile's operands live at a time
+    }
+    if constexpr (kDirect) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        rr[e] = row16_sum(rr[e]);
+        cc[e] = row16_sum(cc[e]);
+      }
+      sds = row16_sum(sds);
+      sds += __shfl_xor(sds, 16);
+      sds += __shfl_xor(sds, 32);
+      if (l16 == 0) {
+        *reinterpret_cast<float4*>(sR + own4) = make_float4(rr[0], rr[1], rr[2], rr[3]);
+        *reinterpret_cast<float4*>(sC + own4) = make_float4(cc[0], cc[1], cc[2], cc[3]);
+      }
+      if (lane == 0) sS[wave] = sds;
+      __syncthreads();
+    }
+    if (wave == 0) {
+      const bool ok = lane < L;
+      float dg = 0.f;
+      if constexpr (kDirect) {
+        float r = 0.f, c = 0.f;
+        if (ok) {
+          r = sR[lane] + (sX[lane] - ((sXc[0][lane] + sXc[1][lane]) + (sXc[2][lane] + sXc[3][lane])));
+          c = sC[lane];
+        }
+        const float c_own = c;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const float x = __shfl_down(r, d), y = __shfl_up(c, d);
+          if (lane + d < 64) r += x;
+          if (lane >= d) c += y;
+        }
+        dg = r + (c - c_own) + sc[kSl * kC] * ((sS[0] + sS[1]) + (sS[2] + sS[3]));
+      } else {
+        const float* tk = ws_tok + ch * (V / 16) * kC + lane;
+#pragma unroll
+        for (int i = 0; i < V / 16; ++i) dg += tk[i * kC];
+      }
+      // before a sequence's first token there is nothing to decay without a state
+      if (geo.c == 0 && lane == 0 && !has_h0) dg = 0.f;
+      float pa = 0.f, pb = 0.f;
+      if (ok) {
+        const int64_t at = (geo.t0 + lane) * HV + hv;
+        float xb, as;
+        const float gn = gdn_gate(gate, at, hv, &xb, &as);
+        const float dx = gate.raw ? -dg * as * sigmoid_f32(xb) : dg;
+        st_any(dgate, at, gate.bf, dx);
+        pa = dg * gn;  // dg / dA_log = g
+        pb = dx;
+      }
+      if (gate.A_log || gate.dt_bias) {
+#pragma unroll
+        for (int d = 32; d; d >>= 1) {
+          pa += __shfl_xor(pa, d);
+          pb += __shfl_xor(pb, d);
+        }
+        if (lane == 0) {
+          par[2 * ch] = pa;
+          par[2 * ch + 1] = pb;
+        }
+      }
+    }
+    if (hh == 0) {
+      rq4 = f32x4{frq[0], frq[1], frq[2], frq[3]};
+      rk4 = f32x4{frk[0], frk[1], frk[2], frk[3]};
+    }
+    __syncthreads();  // sG and sB are rewritten for the next value head
+  }
+
+  // through the L2 norm: q^ = rq q, so dq = rq (dq^ - q^ <q^, dq^>); aq holds rq dq^
+  if (l2) {
+    float nq[4] = {0.f, 0.f, 0.f, 0.f}, nk[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const f32x4 qt = TT::tile(sQ, wave, r), kt = TT::tile(sK, wave, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        nq[e] = fmaf(qt[e], aq[r][e], nq[e]);
+        nk[e] = fmaf(kt[e], ak[r][e], nk[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      nq[e] = row16_sum(nq[e]) * rq4[e] * rq4[e];
+      nk[e] = row16_sum(nk[e]) * rk4[e] * rk4[e];
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const f32x4 qt = TT::tile(sQ, wave, r), kt = TT::tile(sK, wave, r);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        aq[r][e] = fmaf(-qt[e], nq[e], aq[r][e]);
+        ak[r][e] = fmaf(-kt[e], nk[e], ak[r][e]);
+      }
+    }
+  }
+  const int64_t out = (geo.t0 * H + h) * K;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    if constexpr (sizeof(T) == 2) {
+      const int row = own4 + (l16 & 3), col = 32 * (r >> 1) + 8 * (l16 >> 2) + 4 * (r & 1);
+      const uint2 x = quad_transpose(pack4(aq[r])), y = quad_transpose(pack4(ak[r]));
+      if (row < L) {
+        *reinterpret_cast<uint2*>(dq + out + (int64_t)row * H * K + col) = x;
+        *reinterpret_cast<uint2*>(dk + out + (int64_t)row * H * K + col) = y;
+      }
+    } else {
+      const int col = perm_row(r, l16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (own4 + e < L) {
+          dq[out + (int64_t)(own4 + e) * H * K + col] = aq[r][e];
+          dk[out + (int64_t)(own4 + e) * H * K + col] = ak[r][e];
+        }
+    }
+  }
+}
+
+// dA_log[hv], d_dt_bias[hv]: the chunks' partial sums in a fixed order, in double
+__global__ void __launch_bounds__(256)
+gdn_par_kernel(const float* __restrict__ par, const int* __restrict__ table, int chunks, int HV, int bf,
+               void* dA, void* db) {
+  __shared__ double s[2][256];
+  const int hv = blockIdx.x, n = table ? table[0] : chunks;
+  double a = 0., b = 0.;
+  for (int c = threadIdx.x; c < n; c += 256) {
+    const float2 x = reinterpret_cast<const float2*>(par)[(size_t)c * HV + hv];
+    a += x.x;
+    b += x.y;
+  }
+  s[0][threadIdx.x] = a;
+  s[1][threadIdx.x] = b;
+  __syncthreads();
+  for (int d = 128; d; d >>= 1) {
+    if (threadIdx.x < d) {
+      s[0][threadIdx.x] += s[0][threadIdx.x + d];
+      s[1][threadIdx.x] += s[1][threadIdx.x + d];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    if (dA) st_any(dA, hv, bf, (float)s[0][0]);
+    if (db) st_any(db, hv, bf, (float)s[1][0]);
+  }
+}
+
+template <typename T, int K, int V, int NW>
+static hipError_t rev_t(const kda_dims& d, const void* q, const void* k, const void* v, const void* dO,
+                        const float* dht, const int32_t* cu, const GdnLayout<T>& w, void* dv, float* dh0, hipStream_t s) {
+  constexpr size_t lds = GdnRevLds<T, K>::total;
+  static_assert(lds <= 160 * 1024, "LDS");
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_rev_scan_kernel<T, K, V, NW>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((gdn_rev_scan_kernel<T, K, V, NW>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NW)),
+                     dim3(64 * NW), lds, s, (const T*)q, (const T*)k, (const T*)v, (const T*)dO, dht, cu,
+                     w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (T*)dv, dh0, w.dS, w.D, w.tok, w.end);
+  return hipGetLastError();
+}
+
+template <typename T, int K, int V>
+static hipError_t gdn_bwd_kv(const kda_dims& d, const void* q, const void* k, const void* v, const GdnGate& gate, int l2,
+                             const float* h0, const int32_t* cu, const void* dO, const float* dht, void* dq,
+                             void* dk, void* dv, void* dgate, void* dbeta, float* dh0, void* dA,
+                             void* ddt, void* ws, hipStream_t s) {
+  const int64_t mc = max_chunks(d, cu != nullptr);
+  const GdnLayout<T> w(d, cu != nullptr, ws, true);
+  const bool wide = (int64_t)d.N * d.HV * (V / 64) >= kda_host::device_cus();
+  hipError_t e = hipSuccess;
+  if (d.N > 0)
+    e = wide ? rev_t<T, K, V, 4>(d, q, k, v, dO, dht, cu, w, dv, dh0, s)
+             : rev_t<T, K, V, 2>(d, q, k, v, dO, dht, cu, w, dv, dh0, s);
+  if (e != hipSuccess) return e;
+  if (d.N > 0 && mc > 0) {
+    constexpr size_t lds = 2 * TokTile<T, K>::bytes;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_local_kernel<T, K, V>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((gdn_local_kernel<T, K, V>), dim3((unsigned)(mc * d.H)), dim3(256), lds, s,
+                       (const T*)q, (const T*)k, (const T*)dO, gate, cu, w.table, d.N, d.T, d.H, d.HV, l2,
+                       h0 != nullptr ? 1 : 0, 1.0f / sqrtf((float)K), w.scal, w.S0, w.Y, w.dS, w.D, w.tok,
+                       (T*)dq, (T*)dk, (T*)dbeta, dgate, w.par);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (dA || ddt) {
+    hipLaunchKernelGGL(gdn_par_kernel, dim3((unsigned)d.HV), dim3(256), 0, s, w.par,
+                       cu && d.N > 0 ? w.table : (const int*)nullptr, d.N > 0 ? (int)mc : 0, d.HV, gate.bf, dA,
+                       ddt);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace kda
+
+namespace kda_host {
+
+hipError_t launch_gdn_bwd(const kda_dims& d, kda_dtype dt, const void* q, const void* k, const void* v,
+                          const kda::GdnGate& gate, int l2, const float* h0, const int32_t* cu, const void* dO,
+                          const float* dht, void* dq, void* dk, void* dv,
+                          void* dgate, void* dbeta, float* dh0, void* dA, void* ddt, void* ws,
+                          hipStream_t s) {
+#define KDA_GDN_BWD(T_, K_, V_) \
+  if (d.K == K_ && d.V == V_)   \
+    return kda::gdn_bwd_kv<T_, K_, V_>(d, q, k, v, gate, l2, h0, cu, dO, dht, dq, dk, dv, dgate, dbeta, dh0, dA, ddt, ws, s);
+#define KDA_GDN_BWD_ALL(T_)    \
+  KDA_GDN_BWD(T_, 64, 64)      \
+  KDA_GDN_BWD(T_, 64, 128)     \
+  KDA_GDN_BWD(T_, 128, 64)     \
+  KDA_GDN_BWD(T_, 128, 128)
+  if (dt == KDA_BF16) {
+    KDA_GDN_BWD_ALL(kda::bf16)
+  } else {
+    KDA_GDN_BWD_ALL(float)
+  }
+#undef KDA_GDN_BWD_ALL
+#undef KDA_GDN_BWD
+  return hipErrorInvalidValue;
+}
+
+}  // namespace kda_host

@@ -24,6 +24,17 @@ only; every step runs in libkda's kernels).
                                    cu_seqlens, qk_l2norm, conv taps and biases) -> o
       One decode step from raw projections; mutates state and conv_state.
 
+  torch.ops.kda.chunk_gdn_train(q, k, v, gate, beta, A_log, dt_bias, initial_state,
+                                cu_seqlens, raw_gate, qk_l2norm) -> (o, final_state)
+      The scalar-gate chunked forward (gate [B, T, HV]: the raw input with
+      raw_gate, else the natural-log gate), differentiable in every tensor but
+      cu_seqlens (kda_gdn_chunk_fwd, kda_gdn_chunk_bwd).
+  torch.ops.kda.recurrent_gdn_step(q, k, v, gate, beta, A_log, dt_bias, state,
+                                   cu_seqlens, raw_gate, qk_l2norm) -> o
+      Its decode step; mutates state; inference only.
+  torch.ops.kda.gated_norm(x, weight, bias, gate, cu_seqlens, kind, activation, eps) -> y
+      The output norm, differentiable in x, weight, bias and gate.
+
 All have fake (meta) implementations, so they trace under torch.compile and
 FakeTensor. Shapes: q, k [B, T, H, K]; v [B, T, HV, V]; x [B, T, HV, K] FP32;
 beta [B, T, HV]; A_log [HV] FP32; dt_bias [HV, K] FP32; initial_state
@@ -36,8 +47,8 @@ from typing import Optional, Tuple
 import torch
 from torch import Tensor
 
-from . import (chunk_kda, chunk_kda_bwd, conv_state_shape, gate_bwd, gate_cumsum, recurrent_kda,
-               short_conv)
+from . import (chunk_gdn, chunk_gdn_bwd, chunk_kda, chunk_kda_bwd, conv_state_shape, gate_bwd,
+               gate_cumsum, gated_norm, gated_norm_bwd, recurrent_gdn, recurrent_kda, short_conv)
 
 _CHUNK = 64
 
@@ -168,3 +179,73 @@ def _recurrent_kda_step_fake(q, k, v, x, beta, A_log, state, conv_state, cu_seql
                              conv_q_weight, conv_k_weight, conv_v_weight, conv_q_bias, conv_k_bias,
                              conv_v_bias):
     return torch.empty_like(v)
+
+
+@torch.library.custom_op("kda::chunk_gdn_train", mutates_args=(), device_types="cuda")
+def chunk_gdn_train(q: Tensor, k: Tensor, v: Tensor, gate: Tensor, beta: Tensor, A_log: Optional[Tensor],
+                    dt_bias: Optional[Tensor], initial_state: Optional[Tensor],
+                    cu_seqlens: Optional[Tensor], raw_gate: bool, qk_l2norm: bool) -> Tuple[Tensor, Tensor]:
+    return chunk_gdn(q, k, v, gate, beta, initial_state, cu_seqlens=cu_seqlens, output_final_state=True,
+                     use_gate_in_kernel=raw_gate, A_log=A_log, dt_bias=dt_bias, qk_l2norm=qk_l2norm)
+
+
+@chunk_gdn_train.register_fake
+def _chunk_gdn_train_fake(q, k, v, gate, beta, A_log, dt_bias, initial_state, cu_seqlens, raw_gate, qk_l2norm):
+    N = _n_states(q, cu_seqlens)
+    return torch.empty_like(v), q.new_empty((N, v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32)
+
+
+def _gdn_setup(ctx, inputs, output):
+    *tensors, ctx.raw_gate, ctx.qk_l2norm = inputs
+    ctx.save_for_backward(*tensors)
+
+
+def _gdn_backward(ctx, do, dht):
+    q, k, v, gate, beta, A_log, dt_bias, h0, cu = ctx.saved_tensors
+    r = chunk_gdn_bwd(q, k, v, gate, beta, h0, do.contiguous(), dht.contiguous(), cu_seqlens=cu,
+                      use_gate_in_kernel=ctx.raw_gate, A_log=A_log, dt_bias=dt_bias,
+                      qk_l2norm=ctx.qk_l2norm)
+    return (r["dq"], r["dk"], r["dv"], r["dg"], r["dbeta"], r["dA_log"], r["ddt_bias"], r["dh0"], None, None, None)
+
+
+chunk_gdn_train.register_autograd(_gdn_backward, setup_context=_gdn_setup)
+
+
+@torch.library.custom_op("kda::recurrent_gdn_step", mutates_args=("state",), device_types="cuda")
+def recurrent_gdn_step(q: Tensor, k: Tensor, v: Tensor, gate: Tensor, beta: Tensor, A_log: Optional[Tensor],
+                       dt_bias: Optional[Tensor], state: Tensor, cu_seqlens: Optional[Tensor], raw_gate: bool,
+                       qk_l2norm: bool) -> Tensor:
+    return recurrent_gdn(q, k, v, gate, beta, state, cu_seqlens=cu_seqlens, output_final_state=True,
+                         final_state=state, use_gate_in_kernel=raw_gate, A_log=A_log, dt_bias=dt_bias,
+                         qk_l2norm=qk_l2norm)[0]
+
+
+@recurrent_gdn_step.register_fake
+def _recurrent_gdn_step_fake(q, k, v, gate, beta, A_log, dt_bias, state, cu_seqlens, raw_gate, qk_l2norm):
+    return torch.empty_like(v)
+
+
+@torch.library.custom_op("kda::gated_norm", mutates_args=(), device_types="cuda")
+def gated_norm_op(x: Tensor, weight: Optional[Tensor], bias: Optional[Tensor], gate: Optional[Tensor],
+                  cu_seqlens: Optional[Tensor], kind: str, activation: str, eps: float) -> Tensor:
+    return gated_norm(x, weight, bias, gate, kind=kind, activation=activation, eps=eps, cu_seqlens=cu_seqlens)
+
+
+@gated_norm_op.register_fake
+def _gated_norm_fake(x, weight, bias, gate, cu_seqlens, kind, activation, eps):
+    return torch.empty_like(x)
+
+
+def _norm_setup(ctx, inputs, output):
+    x, weight, bias, gate, cu, ctx.kind, ctx.activation, ctx.eps = inputs
+    ctx.save_for_backward(x, weight, bias, gate, cu)
+
+
+def _norm_backward(ctx, dy):
+    x, weight, bias, gate, cu = ctx.saved_tensors
+    r = gated_norm_bwd(x, dy.contiguous(), weight, bias, gate, kind=ctx.kind, activation=ctx.activation,
+                       eps=ctx.eps, cu_seqlens=cu)
+    return r["dx"], r["dweight"], r["dbias"], r["dgate"], None, None, None, None
+
+
+gated_norm_op.register_autograd(_norm_backward, setup_context=_norm_setup)

@@ -523,6 +523,130 @@ kda_status kda_recurrent_fwd_ex(const kda_dims* dims, kda_dtype dtype, const voi
                                 const int32_t* cu_seqlens, int32_t output_final_state, void* o,
                                 float* final_state, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The gated delta rule with ONE decay per value head and token (scalar gate):
+ *   S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T
+ *   o_t = S_t^T (q_t / sqrt(K))
+ * i.e. the sibling gated-delta-rule op of the pages (chunked: kkt, solve_tril,
+ * fwd_h, fwd_o, "[Fix] Use unit KDA gate scale when A_log is omitted", squashed
+ * commit bodies), with its gate activation and q/k L2 norm inside the kernels.
+ * Layouts, varlen packing, empty slots, capacity tail, states and ownership as
+ * in the conventions at the top of this file.
+ */
+
+/* Gate of the scalar-gate entry points. One element type for all three:
+ * KDA_FP32, or KDA_BF16 where q is bf16 as well.
+ *   kind KDA_GATE_NAT  x is the natural-log gate g (A_log, dt_bias NULL);
+ *   kind KDA_GATE_RAW  g = -exp(A_log) * softplus(x + dt_bias) (A_log NULL:
+ *                      unit scale; dt_bias NULL: no bias). KDA_GATE_LOG2 is
+ *                      KDA_ERR_SHAPE. */
+typedef struct {
+  const void* x;        /* [B, T, HV] */
+  const void* A_log;    /* [HV] or NULL */
+  const void* dt_bias;  /* [HV] or NULL */
+  int32_t dtype;        /* kda_dtype of the three */
+  int32_t kind;         /* kda_gate_kind */
+} kda_gdn_gate;
+
+/* Workspace bytes of kda_gdn_chunk_fwd (backward 0) or kda_gdn_chunk_bwd
+ * (backward 1). 0 on invalid or unsupported dims (K and V in {64, 128}). */
+size_t kda_gdn_chunk_workspace_bytes(const kda_dims* dims, kda_dtype dtype, int32_t backward);
+
+/*
+ * kda_gdn_chunk_fwd -- chunked forward (chunks of 64 tokens, matrix cores).
+ *   q, k, v, beta   in `dtype`; qk_l2norm != 0: q and k rows are scaled by
+ *                   1/sqrt(sum x^2 + 1e-6) first (folded into row factors).
+ *   o               [B, T, HV, V] in `dtype`. final_state FP32, may equal
+ *                   initial_state; with bf16 inputs it still has FP32 quality
+ *                   (about 1e-6 relative).
+ * q, k, v, o 16-byte aligned, workspace 256-byte aligned (KDA_ERR_UNSUPPORTED).
+ */
+kda_status kda_gdn_chunk_fwd(const kda_dims* dims, kda_dtype dtype, const void* q, const void* k,
+                             const void* v, const kda_gdn_gate* gate, int32_t qk_l2norm,
+                             const void* beta, const float* initial_state,
+                             const int32_t* cu_seqlens, int32_t output_final_state, void* o,
+                             float* final_state, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/*
+ * kda_gdn_chunk_bwd -- gradients of kda_gdn_chunk_fwd (same inputs).
+ *   do_             [B, T, HV, V]; dht FP32 [N, HV, K, V] or NULL (zeros).
+ *   dq, dk, dv, dbeta  like q, k, v, beta (dq, dk summed over the value heads
+ *                   of a q/k head, in head order; through the L2 norm if set).
+ *   dgate           like gate.x: the gradient of x (of g for KDA_GATE_NAT).
+ *   dA_log, d_dt_bias  [HV] in gate.dtype, given exactly when A_log / dt_bias
+ *                   are; summed in a fixed order.
+ *   dh0             FP32 [N, HV, K, V] or NULL (not wanted).
+ * The chunk states are formed again here, not kept by the forward: they are
+ * larger than the inputs. Outputs must not overlap each other, an input or the workspace.
+ */
+kda_status kda_gdn_chunk_bwd(const kda_dims* dims, kda_dtype dtype, const void* q, const void* k,
+                             const void* v, const kda_gdn_gate* gate, int32_t qk_l2norm,
+                             const void* beta, const float* initial_state,
+                             const int32_t* cu_seqlens, const void* do_, const float* dht, void* dq,
+                             void* dk, void* dv, void* dgate, void* dbeta, float* dh0, void* dA_log,
+                             void* d_dt_bias, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/*
+ * kda_gdn_recurrent_fwd -- token-sequential forward in FP32 (decode, short
+ * sequences; K, V <= 256, any alignment). Arguments as kda_gdn_chunk_fwd; no
+ * workspace. K in {64, 128, 256} with V a multiple of 4 and 16-byte aligned
+ * buffers takes the vectorised kernel.
+ */
+kda_status kda_gdn_recurrent_fwd(const kda_dims* dims, kda_dtype dtype, const void* q,
+                                 const void* k, const void* v, const kda_gdn_gate* gate,
+                                 int32_t qk_l2norm, const void* beta, const float* initial_state,
+                                 const int32_t* cu_seqlens, int32_t output_final_state, void* o,
+                                 float* final_state, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Output norm of the layer (FusedRMSNormGated in the pages' layer imports, and
+ * its layer-norm form), over rows of D:
+ *   mu = mean(x) (KDA_NORM_LAYER; 0 for KDA_NORM_RMS)
+ *   n = (x - mu) / sqrt(mean((x - mu)^2) + eps),  a = n * weight + bias
+ *   y = a * act(gate)      (y = a without a gate)
+ */
+typedef enum { KDA_NORM_RMS = 0, KDA_NORM_LAYER = 1 } kda_norm_kind;
+typedef enum { KDA_ACT_SILU = 0, KDA_ACT_SIGMOID = 1 } kda_norm_act;
+typedef struct {
+  const void* weight;   /* [D] or NULL (ones) */
+  const void* bias;     /* [D] or NULL (zeros) */
+  int32_t param_dtype;  /* kda_dtype of weight and bias: KDA_FP32, or KDA_BF16 for bf16 rows */
+  int32_t D;            /* 1 .. 8192 */
+  int32_t kind;         /* kda_norm_kind */
+  int32_t activation;   /* kda_norm_act, used when a gate is given */
+  float eps;            /* >= 0, finite */
+} kda_norm;
+
+/*
+ * kda_norm_fwd -- x, gate (or NULL) and y are [rows, D] in `dtype`.
+ *   cu_seqlens (device int32 [N + 1], or NULL): only the first cu_seqlens[N] *
+ *   rows_per_token rows are read and written (the capacity tail of a packed
+ *   batch [T, rows_per_token, D] stays as it is); that product must not exceed
+ *   rows. y may be x or gate itself; no other overlap. Any alignment (16-byte
+ *   aligned rows take the vectorised kernel).
+ */
+kda_status kda_norm_fwd(kda_dtype dtype, int64_t rows, const kda_norm* norm,
+                        const int32_t* cu_seqlens, int32_t N, int32_t rows_per_token, const void* x,
+                        const void* gate, void* y, hipStream_t stream);
+
+/* Workspace bytes of kda_norm_bwd when it forms dweight or dbias (0 on an invalid D). */
+size_t kda_norm_bwd_workspace_bytes(const kda_norm* norm);
+
+/*
+ * kda_norm_bwd -- gradients of kda_norm_fwd from dy [rows, D].
+ *   dx [rows, D]; dgate [rows, D] exactly when gate is given; dweight, dbias
+ *   [D] in param_dtype, each exactly when its parameter is given: summed over
+ *   the live rows in FP32 and a fixed order (per-workgroup partials in the
+ *   workspace, 16-byte aligned, then double).
+ *   dx may be x or dy itself, dgate may be gate itself; no other overlap.
+ */
+kda_status kda_norm_bwd(kda_dtype dtype, int64_t rows, const kda_norm* norm,
+                        const int32_t* cu_seqlens, int32_t N, int32_t rows_per_token, const void* x,
+                        const void* gate, const void* dy, void* dx, void* dgate, void* dweight,
+                        void* dbias, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

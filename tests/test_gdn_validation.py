@@ -1,0 +1,194 @@
+"""Refusals of the scalar-gate scan and the output norm, in the binding (before
+anything reaches the library) and in the C ABI (before any launch). CPU only."""
+import ctypes
+
+import pytest
+import torch
+
+import gated_delta_rule_69_amd as kda
+from gated_delta_rule_69_amd.gdn import KdaGdnGate
+from gated_delta_rule_69_amd.norm import KdaNorm
+
+B, T, H, HV, K, V = 1, 10, 2, 4, 64, 64
+BF = torch.bfloat16
+
+
+def _a(dtype=BF, gdt=None):
+    z = torch.zeros
+    return dict(q=z(B, T, H, K, dtype=dtype), k=z(B, T, H, K, dtype=dtype), v=z(B, T, HV, V, dtype=dtype),
+                gate=z(B, T, HV, dtype=gdt or dtype), beta=z(B, T, HV, dtype=dtype), initial_state=z(3, HV, K, V),
+                cu_seqlens=torch.tensor([0, 3, 3, 9], dtype=torch.int32))
+
+
+def _call(fn, a, **kw):
+    args = [a[m] for m in ("q", "k", "v", "gate", "beta", "initial_state")]
+    if fn is kda.chunk_gdn_bwd:
+        args += [kw.pop("do", torch.zeros_like(a["v"])), kw.pop("dht", None)]
+    return fn(*args, cu_seqlens=a["cu_seqlens"], **kw)
+
+
+FNS = [kda.chunk_gdn, kda.recurrent_gdn, kda.chunk_gdn_bwd]
+
+
+@pytest.mark.parametrize("fn", FNS)
+@pytest.mark.parametrize("name,value,err", [
+    ("k", torch.zeros(B, T, H, K), TypeError), ("k", torch.zeros(B, T, H, K - 1, dtype=BF), ValueError),
+    ("v", torch.zeros(B, T, 3, V, dtype=BF), ValueError), ("v", torch.zeros(B, T + 1, HV, V, dtype=BF), ValueError),
+    ("gate", torch.zeros(B, T, HV, K, dtype=BF), ValueError), ("gate", torch.zeros(B, T, HV, dtype=torch.float16), TypeError),
+    ("beta", torch.zeros(B, T, HV), TypeError), ("initial_state", torch.zeros(2, HV, K, V), ValueError),
+    ("initial_state", torch.zeros(3, HV, K, V, dtype=BF), TypeError),
+    ("cu_seqlens", torch.tensor([0, 3, 3, 9]), TypeError), ("cu_seqlens", torch.zeros(2, 2, dtype=torch.int32), ValueError),
+    ("q", torch.zeros(B, T, H, K, dtype=torch.float16), TypeError), ("q", torch.zeros(T, H, K, dtype=BF), ValueError),
+    ("q", None, TypeError), ("gate", None, TypeError)])
+def test_scan_arguments(fn, name, value, err):
+    a = _a()
+    a[name] = value
+    with pytest.raises(err):
+        _call(fn, a)
+
+
+@pytest.mark.parametrize("fn", FNS)
+def test_scan_layouts_parameters_and_device(fn):
+    a = _a()
+    a["q"] = torch.zeros(B, H, T, K, dtype=BF).transpose(1, 2)
+    with pytest.raises(ValueError, match="contiguous"):
+        _call(fn, a)
+    with pytest.raises(ValueError, match="use_gate_in_kernel"):
+        _call(fn, _a(), A_log=torch.zeros(HV, dtype=BF))
+    with pytest.raises(TypeError, match="A_log"):  # one dtype for the gate and its parameters
+        _call(fn, _a(), use_gate_in_kernel=True, A_log=torch.zeros(HV))
+    with pytest.raises(TypeError, match="gate"):  # a bf16 gate needs bf16 inputs
+        _call(fn, _a(torch.float32, BF))
+    with pytest.raises(ValueError, match="device tensor"):
+        _call(fn, _a())
+
+
+def test_scan_misuse():
+    a = _a()
+    a["q"].requires_grad_()
+    with pytest.raises(RuntimeError, match="inference"):
+        _call(kda.recurrent_gdn, a)
+    with pytest.raises(TypeError, match="do"):
+        _call(kda.chunk_gdn_bwd, _a(), do=None)
+    with pytest.raises(ValueError, match="dht"):
+        _call(kda.chunk_gdn_bwd, _a(), dht=torch.zeros(2, HV, K, V))
+
+
+@pytest.mark.parametrize("kw,err", [
+    (dict(kind="batch"), ValueError), (dict(activation="relu"), ValueError), (dict(weight=torch.zeros(7)), ValueError),
+    (dict(weight=torch.zeros(8, dtype=torch.float16)), TypeError), (dict(gate=torch.zeros(4, 8)), TypeError),
+    (dict(gate=torch.zeros(4, 9, dtype=BF)), ValueError),
+    (dict(weight=torch.zeros(8), bias=torch.zeros(8, dtype=BF)), TypeError),
+    (dict(cu_seqlens=torch.zeros(2, dtype=torch.int32)), ValueError), (dict(), ValueError)])
+def test_norm_arguments(kw, err):
+    with pytest.raises(err):
+        kda.gated_norm(torch.zeros(4, 8, dtype=BF), **kw)
+    kw = dict(kw)
+    with pytest.raises(err):
+        kda.gated_norm_bwd(torch.zeros(4, 8, dtype=BF), torch.zeros(4, 8, dtype=BF), **kw)
+
+
+def test_norm_misuse():
+    with pytest.raises(TypeError):
+        kda.gated_norm(torch.zeros(4, 8, dtype=torch.float64))
+    with pytest.raises(ValueError):
+        kda.gated_norm(torch.zeros(8, 4, dtype=BF).t())
+    with pytest.raises(TypeError):
+        kda.gated_norm_bwd(torch.zeros(4, 8), None)
+
+
+P = [ctypes.c_void_p(0x1000000 * (i + 1)) for i in range(24)]  # never dereferenced
+
+
+def _dims(**kw):
+    d = dict(B=1, T=64, N=1, H=1, HV=1, K=64, V=64)
+    d.update(kw)
+    return kda.KdaDims(**d)
+
+
+def _gate(kind=2, dtype=1, x=0x70000000, A=None, b=None):
+    return KdaGdnGate(x, A, b, dtype, kind)
+
+
+def _fwd(d, g, dt=1, o=P[5], ht=P[6], h0=None, ws=P[7], wb=1 << 40, cu=None, fin=1, q=P[0]):
+    return kda.load().kda_gdn_chunk_fwd(ctypes.byref(d), dt, q, P[1], P[2], ctypes.byref(g), 0, P[4], h0, cu, fin, o,
+                                        ht, ws, wb, None)
+
+
+def _rec(d, g, dt=1, o=P[5], ht=P[6], h0=None, cu=None, fin=1):
+    return kda.load().kda_gdn_recurrent_fwd(ctypes.byref(d), dt, P[0], P[1], P[2], ctypes.byref(g), 0, P[4], h0, cu,
+                                            fin, o, ht, None)
+
+
+def test_abi_scan_refusals():
+    lib = kda.load()
+    for f in (_fwd, _rec):
+        assert f(_dims(H=2, HV=3), _gate()) == 2
+        assert f(_dims(N=2), _gate()) == 2
+        assert f(_dims(B=2, N=2), _gate(), cu=P[9]) == 2
+        assert f(_dims(), _gate(), dt=5) == 3
+        assert f(_dims(), _gate(dtype=1), dt=0) == 3  # bf16 gate, FP32 inputs
+        assert f(_dims(), _gate(kind=0)) == 2  # no log2 gates here
+        assert f(_dims(), _gate(kind=1, A=0x10)) == 2
+        assert f(_dims(), _gate(x=None)) == 1
+        assert f(_dims(), _gate(), ht=None) == 1
+        assert f(_dims(), _gate(), o=P[0]) == 5  # o over q
+        assert f(_dims(), _gate(), o=ctypes.c_void_p(0x70000000)) == 5  # o over the gate
+        assert f(_dims(), _gate(), h0=P[6], ht=ctypes.c_void_p(P[6].value + 64)) == 5
+    assert _fwd(_dims(K=80), _gate()) == 4 and _fwd(_dims(V=32), _gate()) == 4
+    assert _rec(_dims(K=300), _gate()) == 4
+    assert _fwd(_dims(), _gate(), q=ctypes.c_void_p(P[0].value + 2)) == 4
+    assert _fwd(_dims(), _gate(), ws=ctypes.c_void_p(P[7].value + 16)) == 4
+    assert _fwd(_dims(), _gate(), ws=None) == 6
+    need = lib.kda_gdn_chunk_workspace_bytes(ctypes.byref(_dims()), 1, 0)
+    more = lib.kda_gdn_chunk_workspace_bytes(ctypes.byref(_dims()), 1, 1)
+    assert 0 < need < more
+    assert _fwd(_dims(), _gate(), wb=need - 1) == 6 and _bwd(_dims(), _gate(), wb=more - 1) == 6
+    assert lib.kda_gdn_chunk_workspace_bytes(ctypes.byref(_dims(K=65)), 1, 0) == 0
+    assert lib.kda_gdn_chunk_fwd(None, 1, *[None] * 3, None, 0, None, None, None, 0, None, None, None, 0, None) == 1
+
+
+def _bwd(d, g, dt=1, dA=None, db=None, dq=P[8], dh0=None, ws=P[15], wb=1 << 40, do=P[7]):
+    return kda.load().kda_gdn_chunk_bwd(ctypes.byref(d), dt, P[0], P[1], P[2], ctypes.byref(g), 0, P[4], None, None,
+                                        do, None, dq, P[9], P[10], P[11], P[12], dh0, dA, db, ws, wb, None)
+
+
+def test_abi_backward_refusals():
+    assert _bwd(_dims(), _gate(A=0x60000000)) == 2  # A_log without dA_log
+    assert _bwd(_dims(), _gate(), dA=P[13]) == 2
+    assert _bwd(_dims(), _gate(), db=P[13]) == 2
+    assert _bwd(_dims(), _gate(), dq=P[0]) == 5 and _bwd(_dims(), _gate(), dq=P[9]) == 5
+    assert _bwd(_dims(), _gate(), do=None) == 1 and _bwd(_dims(), _gate(), dq=None) == 1
+    assert _bwd(_dims(), _gate(), ws=None) == 6 and _bwd(_dims(), _gate(), wb=100) == 6
+    assert _bwd(_dims(K=96), _gate()) == 4
+
+
+def _norm(rows=4, dt=1, D=64, pd=0, kind=0, act=0, eps=1e-5, w=None, b=None, x=P[0], z=None, y=P[1], cu=None, N=0,
+          rpt=1):
+    p = KdaNorm(w, b, pd, D, kind, act, eps)
+    return kda.load().kda_norm_fwd(dt, rows, ctypes.byref(p), cu, N, rpt, x, z, y, None)
+
+
+def test_abi_norm_refusals():
+    assert _norm(dt=4) == 3 and _norm(pd=9) == 3 and _norm(dt=0, pd=1) == 3
+    assert _norm(rows=-1) == 2 and _norm(D=0) == 2 and _norm(kind=2) == 2 and _norm(act=2) == 2
+    assert _norm(eps=-1.0) == 2 and _norm(eps=float("nan")) == 2 and _norm(eps=float("inf")) == 2
+    assert _norm(D=8193) == 4
+    assert _norm(x=None) == 1 and _norm(y=None) == 1
+    assert _norm(cu=P[5], N=1, rpt=0) == 2
+    assert _norm(y=ctypes.c_void_p(P[0].value + 8)) == 5 and _norm(w=P[1].value) == 5
+    assert _norm(rows=0, x=None, y=None) == 0
+
+
+def _norm_b(rows=4, D=64, w=None, b=None, z=None, dx=P[2], dz=None, dw=None, db=None, ws=P[9], wb=1 << 40):
+    p = KdaNorm(w, b, 0, D, 0, 0, 1e-5)
+    return kda.load().kda_norm_bwd(1, rows, ctypes.byref(p), None, 0, 1, P[0], z, P[1], dx, dz, dw, db, ws, wb, None)
+
+
+def test_abi_norm_backward_refusals():
+    assert _norm_b(w=P[5].value) == 2 and _norm_b(dw=P[6]) == 2 and _norm_b(z=P[7]) == 2
+    assert _norm_b(dx=None) == 1
+    assert _norm_b(w=P[5].value, dw=P[6], ws=None) == 6 and _norm_b(w=P[5].value, dw=P[6], wb=16) == 6
+    assert _norm_b(w=P[5].value, dw=P[6], ws=ctypes.c_void_p(P[9].value + 4)) == 4
+    assert _norm_b(w=P[5].value, dw=P[2]) == 5
+    assert _norm_b(z=P[7], dz=P[2]) == 5

@@ -1,0 +1,394 @@
+"""GPU parity of the scalar-gate delta rule (chunk_gdn, chunk_gdn_bwd,
+recurrent_gdn) against the FP64 oracle.
+
+Tolerances (norm of the difference over the norm of the result):
+  FP32: 2e-5, the repository's FP32 bar.
+  bf16 outputs: a rounding is off by at most 2^-8 of the value and on average
+    over mantissas and directions by 2^-9.2 (rms). o sees the rounding of the
+    output, of S0's high part and of P (independent): sqrt(3) 2^-9.2 = 3.0e-3;
+    the bar is the repository's 5e-3. dq and dk see the output's rounding and
+    two operands of each of their parts: the repository's 1e-2 bar for bf16
+    gradients, 5e-3 for dv (output rounding; its operands are split).
+  States and state gradients with bf16 inputs: every operand that feeds them
+    is hi + lo, off by at most 2^-16, and a chunk step chains four such
+    roundings (S, b R, M, the update): 4 x 2^-16 = 6.1e-5.
+  The recurrent kernel computes in FP32: state 2e-5, o 2^-8 for its one rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_69_amd as kda
+import gdn_cases as G
+from helpers import DEV
+
+pytestmark = pytest.mark.gpu
+
+FP32, O16, G16, DV16, S16 = 2e-5, 5e-3, 1e-2, 5e-3, 4 * 2.0 ** -16
+
+
+def _bits(t):
+    return t.contiguous().view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32)
+
+
+def _fwd(c, d, fn=kda.chunk_gdn, **kw):
+    return fn(*G.scan_args(d), output_final_state=True, **G.scan_kw(c, d), **kw)
+
+
+def _check_fwd(c, fn=kda.chunk_gdn):
+    d = G.device(c)
+    o, ht = _fwd(c, d, fn)
+    ro, rh = G.forward(c)
+    bf = c["dtype"] == "bf16"
+    rec = fn is kda.recurrent_gdn
+    assert G.rel(o, ro, G.inside(c)) <= ((2.0 ** -8 if rec else O16) if bf else FP32)
+    # state by state, so that one bad chain cannot hide
+    for n in range(c["N"]):
+        assert G.rel(ht[n], rh[n]) <= (S16 if bf and not rec else FP32), n
+
+
+CASES = [
+    dict(lens=[1]), dict(lens=[64]), dict(lens=[65]), dict(lens=[3, 0, 70, 130, 0]),
+    dict(lens=[200, 1, 63], tail=9, l2norm=True), dict(lens=[150, 150], dense=True, H=3, HV=3),
+    dict(lens=[77, 300], K=128, V=128, H=1, HV=4, l2norm=True), dict(lens=[129], K=128, V=64, gate="log"),
+    dict(lens=[90, 40], K=64, V=128, params=False, h0=False), dict(lens=[1, 1, 1], gate="log", h0=False),
+    dict(lens=[257], dense=True, K=128, V=128, H=2, HV=2, h0=False), dict(lens=[100], gate_bf16=False),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_chunk_forward(i, dtype):
+    _check_fwd(G.make(100 + i, dtype=dtype, **CASES[i]))
+
+
+REC = CASES + [dict(lens=[5, 0, 2], K=80, V=24), dict(lens=[3], K=7, V=5, H=1, HV=3),
+               dict(lens=[2, 4], K=256, V=256, H=1, HV=1), dict(lens=[2], K=256, V=100, H=1, HV=2, l2norm=True),
+               dict(lens=[1] * 40, K=128, V=128, H=16, HV=32)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("i", range(len(REC)))
+def test_recurrent_forward(i, dtype):
+    _check_fwd(G.make(200 + i, dtype=dtype, **REC[i]), kda.recurrent_gdn)
+
+
+def _check_bwd(c, **kw):
+    d = G.device(c)
+    r = kda.chunk_gdn_bwd(*G.scan_args(d), d["do"], d["dht"], **G.scan_kw(c, d), **kw)
+    ref = G.backward(c)
+    bf = c["dtype"] == "bf16"
+    for m in ("dq", "dk", "dv", "dg", "dbeta", "dA_log", "ddt_bias", "dh0"):
+        if ref[m] is None:
+            assert r[m] is None
+            continue
+        tol = {"dv": DV16, "dh0": S16}.get(m, G16) if bf else FP32
+        mask = None if m in ("dA_log", "ddt_bias", "dh0") else G.inside(c)
+        assert G.rel(r[m], ref[m], mask) <= tol, (m, G.rel(r[m], ref[m], mask))
+    if not c["dense"]:
+        for m in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert (r[m][:, c["total"]:] == 0).all()
+    return r
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_chunk_backward(i, dtype):
+    _check_bwd(G.make(300 + i, dtype=dtype, **CASES[i]))
+
+
+def test_gradients_against_differences():
+    """Directional derivatives of the FP64 forward, central differences with
+    h = 1e-5 (their error, h^2 and 1e-16 / h relative, is far below the FP32
+    kernel's 2e-5)."""
+    c = G.make(7, [3, 70], dtype="fp32", H=1, HV=2, l2norm=True)
+    d = G.device(c)
+    r = kda.chunk_gdn_bwd(*G.scan_args(d), d["do"], d["dht"], **G.scan_kw(c, d))
+    rng = np.random.default_rng(3)
+
+    def loss(over):
+        o, ht = G.forward(dict(c, **over))
+        return (o * c["do"]).sum() + (ht * c["dht"]).sum()
+
+    names = dict(q="dq", k="dk", v="dv", x="dg", beta="dbeta", h0="dh0", A_log="dA_log", dt_bias="ddt_bias")
+    for m, gm in names.items():
+        a = c[m].astype(np.float64)
+        u = rng.standard_normal(a.shape)
+        h = 1e-5
+        num = (loss({m: a + h * u}) - loss({m: a - h * u})) / (2 * h)
+        got = float((r[gm].double().cpu().numpy() * u).sum())
+        scale = float(np.linalg.norm(r[gm].double().cpu().numpy()) * np.linalg.norm(u))
+        assert abs(num - got) <= 2e-5 * max(scale, 1.0), (m, num, got)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_what_the_workspace_held_before_does_not_matter(dtype):
+    """NaN-filled workspaces give bitwise the results of zeroed ones, twice."""
+    c = G.make(8, [70, 0, 129], dtype=dtype, K=128, V=64, H=1, HV=2, tail=5, l2norm=True)
+    d = G.device(c)
+    runs = []
+    for fill in (255, 0, 255):  # 255: NaN in every format
+        ws = [torch.full((kda.chunk_gdn_workspace_bytes(d["q"], d["v"], d["cu"], backward=b),), fill,
+                         dtype=torch.uint8, device=DEV) for b in (False, True)]
+        o, ht = _fwd(c, d, workspace=ws[0])
+        r = kda.chunk_gdn_bwd(*G.scan_args(d), d["do"], d["dht"], workspace=ws[1], **G.scan_kw(c, d))
+        runs.append([o[:, :c["total"]], ht] + list(r.values()))
+    for other in runs[1:]:
+        for i, (a, b) in enumerate(zip(runs[0], other)):
+            assert torch.equal(_bits(a), _bits(b)), i
+
+
+@pytest.mark.parametrize("fn", [kda.chunk_gdn, kda.recurrent_gdn])
+@pytest.mark.parametrize("h0", [True, False])
+def test_empty_slots_tail_and_in_place_state(fn, h0):
+    c = G.make(9, [0, 65, 0, 4, 0], tail=7, h0=h0)
+    d = G.device(c)
+    o = torch.full_like(d["v"], 7.0)
+    before = None if d["h0"] is None else d["h0"].clone()
+    _, ht = fn(*G.scan_args(d), output_final_state=True, o=o, **G.scan_kw(c, d))
+    assert (o[:, c["total"]:] == 7.0).all()
+    for n in (0, 2, 4):
+        want = torch.zeros_like(ht[n]) if before is None else before[n]
+        assert torch.equal(_bits(ht[n]), _bits(want))
+    if h0:
+        st = d["h0"]
+        fn(d["q"], d["k"], d["v"], d["x"], d["beta"], st, output_final_state=True, final_state=st, **G.scan_kw(c, d))
+        assert torch.equal(_bits(st), _bits(ht))
+
+
+@pytest.mark.parametrize("fn", [kda.chunk_gdn, kda.recurrent_gdn])
+def test_all_empty_and_no_tokens(fn):
+    c = G.make(10, [0, 0], tail=3)
+    d = G.device(c)
+    _, ht = _fwd(c, d, fn)
+    assert torch.equal(_bits(ht), _bits(d["h0"]))
+    c = G.make(11, [0, 0], dense=True)
+    d = G.device(c)
+    o, ht = _fwd(c, d, fn)
+    assert o.shape == (2, 0, 4, 64) and torch.equal(_bits(ht), _bits(d["h0"]))
+    if fn is kda.chunk_gdn:
+        r = kda.chunk_gdn_bwd(*G.scan_args(d), d["do"], d["dht"], **G.scan_kw(c, d))
+        assert torch.equal(_bits(r["dh0"]), _bits(d["dht"]))
+        assert (r["dA_log"] == 0).all() and (r["ddt_bias"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_zero_beta_one_beta_and_extreme_gates(dtype):
+    """beta exactly 0 (nothing written, Y still defined) and 1; gates of 0 (no
+    decay), of the size that underflows at once, and a growing gate."""
+    c = G.make(12, [150, 70], dtype=dtype, gate="log", H=1, HV=4)
+    rng = np.random.default_rng(0)
+    c["beta"][0, rng.random(220) < 0.3] = 0.0
+    c["beta"][0, rng.random(220) < 0.2] = 1.0
+    c["x"][..., 0] = 0.0
+    c["x"][..., 1] = G.NEG
+    c["x"][..., 2] = np.where(np.arange(220) % 9 == 4, G.NEG, -0.01)
+    c["x"][..., 3] = 0.01
+    c["x"] = G.rnd(c["gate_dtype"], c["x"])
+    _check_fwd(c)
+    _check_fwd(c, kda.recurrent_gdn)
+    _check_bwd(c)
+
+
+def test_chunk_agrees_with_the_per_channel_kernel():
+    """The same scan through chunk_kda with the gate repeated over the channels."""
+    c = G.make(13, [300, 65], dtype="fp32", gate="log")
+    d = G.device(c)
+    o, ht = _fwd(c, d)
+    wide = d["x"][..., None].expand(-1, -1, -1, c["K"]).contiguous()
+    o2, ht2 = kda.chunk_kda(d["q"], d["k"], d["v"], wide, d["beta"], d["h0"], cu_seqlens=d["cu"],
+                            output_final_state=True, use_gate_in_kernel=True, gate_is_raw=False)
+    assert G.rel(o, o2.cpu().numpy()) <= 2 * FP32 and G.rel(ht, ht2.cpu().numpy()) <= 2 * FP32
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_prefill_in_pieces_then_decode(dtype):
+    """A sequence in two chunked pieces and three decode steps, states handed
+    over, against the whole-sequence oracle."""
+    c = G.make(14, [134], dtype=dtype, K=128, V=128, H=1, HV=2, l2norm=True)
+    d = G.device(c)
+    ro, rh = G.forward(c)
+    st, outs, at = d["h0"], [], 0
+    for n, fn in ((61, kda.chunk_gdn), (70, kda.chunk_gdn), (1, kda.recurrent_gdn), (1, kda.recurrent_gdn),
+                  (1, kda.recurrent_gdn)):
+        cut = {m: d[m][:, at:at + n].contiguous() for m in ("q", "k", "v", "x", "beta")}
+        kw = dict(G.scan_kw(c, d), cu_seqlens=None)
+        o, st = fn(cut["q"], cut["k"], cut["v"], cut["x"], cut["beta"], st, output_final_state=True, **kw)
+        outs.append(o)
+        at += n
+    bf = dtype == "bf16"
+    assert G.rel(torch.cat(outs, 1), ro) <= (O16 if bf else FP32)
+    assert G.rel(st, rh) <= (S16 if bf else FP32)
+
+
+def _capture(fn):
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fn()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = fn()
+    return g, out
+
+
+def test_graph_replays_with_new_inputs_and_boundaries():
+    """Forward, backward and decode captured once and replayed with
+    new inputs and new sequence boundaries; every replay bitwise the eager call."""
+    cs = [G.make(20 + i, lens, K=64, V=64, h0=True, tail=t) for i, (lens, t) in
+          enumerate([([70, 5, 0, 30], 3), ([0, 64, 40, 1], 3), ([1, 1, 105, 1], 0)])]
+    d = G.device(cs[0])
+
+    def step(d):
+        kw = G.scan_kw(cs[0], d)
+        o, ht = kda.chunk_gdn(*G.scan_args(d), output_final_state=True, **kw)
+        r = kda.chunk_gdn_bwd(*G.scan_args(d), d["do"], d["dht"], **kw)
+        o2, ht2 = kda.recurrent_gdn(*G.scan_args(d), output_final_state=True, **kw)
+        return [o, ht, o2, ht2] + list(r.values())
+
+    g, out = _capture(lambda: step(d))
+    for c in cs + cs[:1]:
+        e = G.device(c)
+        for m in d:
+            d[m].copy_(e[m])
+        g.replay()
+        torch.cuda.synchronize()
+        eager = step(e)
+        for i, (a, b) in enumerate(zip(out, eager)):
+            if i in (0, 2):
+                a, b = a[:, :c["total"]], b[:, :c["total"]]
+            assert torch.equal(_bits(a), _bits(b)), i
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own buffers, give what they give alone."""
+    cs = [G.make(30 + i, [400, 100], K=128, V=128) for i in range(2)]
+    ds = [G.device(c) for c in cs]
+    alone = [_fwd(c, d) for c, d in zip(cs, ds)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    outs = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i] = _fwd(cs[i], ds[i])
+    torch.cuda.synchronize()
+    for a, b in zip(alone, outs):
+        assert torch.equal(_bits(a[0]), _bits(b[0])) and torch.equal(_bits(a[1]), _bits(b[1]))
+
+
+def test_one_long_sequence_and_many_heads():
+    _check_fwd(G.make(40, [2000], K=128, V=128, H=1, HV=1, step=(1e-4, 1e-2)))
+    _check_bwd(G.make(41, [1000, 30], K=128, V=128, H=1, HV=2, step=(1e-4, 1e-2)))
+    # enough chains for the 64-column scans and a grouped intra kernel
+    _check_fwd(G.make(42, [40] * 20, K=64, V=64, H=8, HV=16))
+    _check_bwd(G.make(43, [40] * 20, K=64, V=64, H=8, HV=16))
+
+
+def test_offsets_past_32_bits():
+    """q, k, v of more than 2^31 elements each: the last short sequence of the
+    batch gives bitwise what it gives alone."""
+    H = HV = 128
+    K = V = 128
+    T = (1 << 17) + 200
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    q = torch.empty(1, T, H, K, device=DEV, dtype=torch.bfloat16).normal_(generator=g)
+    v = torch.empty(1, T, HV, V, device=DEV, dtype=torch.bfloat16).normal_(generator=g)
+    x = torch.empty(1, T, HV, device=DEV, dtype=torch.bfloat16).normal_(generator=g)
+    beta = torch.sigmoid(x)
+    first = T - 150
+    # the long part is many short sequences, so that the call stays short
+    cuts = list(range(0, first, 4096)) + [first, T]
+    cu = torch.tensor(cuts, dtype=torch.int32, device=DEV)
+    kw = dict(output_final_state=True, use_gate_in_kernel=True, qk_l2norm=True)
+    o, ht = kda.chunk_gdn(q, q, v, x, beta, cu_seqlens=cu, **kw)
+    cut = [t[:, first:].contiguous() for t in (q, v, x, beta)]
+    o1, h1 = kda.chunk_gdn(cut[0], cut[0], cut[1], cut[2], cut[3], **kw)
+    assert torch.equal(_bits(o[:, first:]), _bits(o1)) and torch.equal(_bits(ht[-1]), _bits(h1[0]))
+    w = torch.ones(V, device=DEV)
+    y = kda.gated_norm(o, w, None, v, kind="rms")
+    y1 = kda.gated_norm(o1, w, None, cut[1], kind="rms")
+    assert torch.equal(_bits(y[:, first:]), _bits(y1))
+
+
+def test_layer_run_together():
+    """What a layer does: short convolution, scan, gated norm; then a decode
+    step continuing history and state, all against FP64."""
+    import oracle
+    rng = np.random.default_rng(4)
+    H, HV, K, V, T, W = 2, 4, 64, 64, 90, 4
+    c = G.make(50, [T - 1], H=H, HV=HV, K=K, V=V, l2norm=True, h0=False)
+    full = G.make(50, [T], H=H, HV=HV, K=K, V=V, l2norm=True, h0=False)
+    d = G.device(full)
+    taps = tuple((torch.from_numpy(rng.uniform(-.5, .5, (D, W)).astype(np.float32)).to(DEV),
+                  torch.from_numpy(rng.uniform(-.5, .5, D).astype(np.float32)).to(DEV))
+                 for D in (H * K, H * K, HV * V))
+    z = torch.randn(1, T, HV, V, device=DEV).bfloat16()
+    w = torch.rand(V, device=DEV) + 0.5
+    cut = {m: d[m][:, :T - 1].contiguous() for m in ("q", "k", "v", "x", "beta")}
+    hist = torch.zeros(kda.conv_state_shape(cut["q"], cut["v"], None, W), device=DEV, dtype=torch.bfloat16)
+    (q, k, v), _ = kda.short_conv(cut["q"], cut["k"], cut["v"], taps, conv_state_out=hist)
+    kw = dict(use_gate_in_kernel=True, A_log=d["A_log"], dt_bias=d["dt_bias"], qk_l2norm=True)
+    o, st = kda.chunk_gdn(q, k, v, cut["x"], cut["beta"], output_final_state=True, **kw)
+    y = kda.gated_norm(o, w, None, z[:, :T - 1].contiguous())
+    one = {m: d[m][:, T - 1:].contiguous() for m in ("q", "k", "v", "x", "beta")}
+    (q, k, v), _ = kda.short_conv(one["q"], one["k"], one["v"], taps, conv_state=hist, conv_state_out=hist)
+    o1, _ = kda.recurrent_gdn(q, k, v, one["x"], one["beta"], st, output_final_state=True, final_state=st, **kw)
+    y1 = kda.gated_norm(o1, w, None, z[:, T - 1:].contiguous())
+    # FP64: convolution outputs rounded to bf16 as the operator returns them
+    cv = []
+    for m, (tw, tb) in zip(("q", "k", "v"), taps):
+        a = full[m].reshape(1, T, -1)
+        cv.append(G.round_bf16(oracle.short_conv_silu(a, tw.cpu().numpy(), tb.cpu().numpy(), None)
+                               .astype(np.float32)).reshape(full[m].shape))
+    ro, rh = G.forward(dict(full, q=cv[0], k=cv[1], v=cv[2]))
+    zz = z.double().cpu().numpy()
+    n = ro / np.sqrt((ro ** 2).mean(-1, keepdims=True) + 1e-5)
+    ry = n * w.double().cpu().numpy() * zz / (1 + np.exp(-zz))
+    # a convolution value next to a rounding border may round the other way
+    # (2^-7 of it, in few of them); o's 5e-3 and the norm's two roundings of 2^-8
+    assert G.rel(torch.cat([y, y1], 1), ry) <= O16 + 2 * 2.0 ** -8
+    assert G.rel(st, rh) <= 2.0 ** -8
+
+
+def test_torch_ops_autograd():
+    import gated_delta_rule_69_amd.torch_ops  # noqa: F401
+    c = G.make(60, [70, 33], dtype="fp32", H=1, HV=2, l2norm=True)
+    d = G.device(c)
+    names = ("q", "k", "v", "x", "beta", "A_log", "dt_bias", "h0")
+    leaf = {m: d[m].clone().requires_grad_() for m in names}
+    o, ht = torch.ops.kda.chunk_gdn_train(leaf["q"], leaf["k"], leaf["v"], leaf["x"], leaf["beta"], leaf["A_log"],
+                                          leaf["dt_bias"], leaf["h0"], d["cu"], True, True)
+    ((o * d["do"]).sum() + (ht * d["dht"]).sum()).backward()
+    ref = G.backward(c)
+    for m, gm in zip(names, ("dq", "dk", "dv", "dg", "dbeta", "dA_log", "ddt_bias", "dh0")):
+        assert G.rel(leaf[m].grad, ref[gm]) <= FP32, m
+    st = d["h0"].clone()
+    o1 = torch.ops.kda.recurrent_gdn_step(d["q"], d["k"], d["v"], d["x"], d["beta"], d["A_log"], d["dt_bias"], st,
+                                          d["cu"], True, True)
+    ro, rh = G.forward(c)
+    assert G.rel(o1, ro) <= FP32 and G.rel(st, rh) <= FP32
+    torch.library.opcheck(torch.ops.kda.chunk_gdn_train.default,
+                          (d["q"], d["k"], d["v"], d["x"], d["beta"], d["A_log"], d["dt_bias"], d["h0"], d["cu"],
+                           True, True))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_shapes(seed):
+    r = np.random.default_rng(1000 + seed)
+    H = int(r.choice([1, 2, 3]))
+    dense = bool(r.random() < 0.3)
+    lens = [int(r.integers(1, 260))] * int(r.integers(1, 4)) if dense else \
+        [int(x) for x in r.choice([0, 1, 2, 63, 64, 65, 127, 190], size=r.integers(1, 6))]
+    if sum(lens) == 0:
+        lens[0] = 5
+    c = G.make(seed, lens, dtype=str(r.choice(["bf16", "fp32"])), dense=dense, H=H, HV=H * int(r.choice([1, 2, 3])),
+               K=int(r.choice([64, 128])), V=int(r.choice([64, 128])), gate=str(r.choice(["raw", "log"])),
+               params=bool(r.random() < 0.5), l2norm=bool(r.random() < 0.5), h0=bool(r.random() < 0.5),
+               tail=0 if dense else int(r.integers(0, 20)), step=(1e-3, float(r.choice([0.01, 0.3, 3.0]))))
+    _check_fwd(c)
+    _check_bwd(c)
+    _check_fwd(c, kda.recurrent_gdn)
