@@ -630,7 +630,9 @@ kda_status gdn_gate_args(const kda_dims* d, kda_dtype dt, const kda_gdn_gate* g,
 }
 
 bool gdn_chunk_supported(const kda_dims* d) {
-  return (d->K == 64 || d->K == 128) && (d->V == 64 || d->V == 128);
+  // 64 tokens' rows of q or v span less than 2^31 bytes (the kernels' 32-bit offsets)
+  return (d->K == 64 || d->K == 128) && (d->V == 64 || d->V == 128) &&
+         (int64_t)d->H * d->K < (1 << 23) && (int64_t)d->HV * d->V < (1 << 23);
 }
 
 // Buffers of one call: every output is checked against every input and every

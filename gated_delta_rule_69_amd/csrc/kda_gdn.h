@@ -135,18 +135,62 @@ __device__ __forceinline__ f32x4 mma8h(const Op8<float>& a, const Op8s<float>& b
   return mma8s(a, b, c);
 }
 
+// Nothing is scheduled across: reads placed before it stay before it.
+__device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
+// c[t] += a[t] b for four row tiles, b split: low parts first, so that the
+// four tiles' steps lie between two steps of one tile
+__device__ __forceinline__ void mma_rows(const Op8<bf16> (&a)[4], const Op8s<bf16>& b, f32x4 (&c)[4]) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t].v, b.lo, c[t], 0, 0, 0);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[t].v, b.hi, c[t], 0, 0, 0);
+}
+// c += X b with the triangular X's six fragments (frag_low order; PT parts:
+// hi, then lo, whose product with b's low part is left out) and b split
+template <int PT, int PX>
+__device__ __forceinline__ void mma_tri(const Op8<bf16> (&a)[PX][6], const Op8s<bf16> (&b)[2], f32x4 (&c)[4]) {
+  static_assert(PT <= PX, "parts");
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int t = 2 * s; t < 4; ++t)
+      c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[0][frag_low(t, s)].v, b[s].lo, c[t], 0, 0, 0);
+    if constexpr (PT == 2) {
+#pragma unroll
+      for (int t = 2 * s; t < 4; ++t)
+        c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[1][frag_low(t, s)].v, b[s].hi, c[t], 0, 0, 0);
+    }
+#pragma unroll
+    for (int t = 2 * s; t < 4; ++t)
+      c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[0][frag_low(t, s)].v, b[s].hi, c[t], 0, 0, 0);
+  }
+}
+// two floats as bf16 in one register (first in the low half), and their rest
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const bf16x2 h = {(bf16)a, (bf16)b};
+  return __builtin_bit_cast(uint32_t, h);
+}
+// a - hi.low and b - hi.high (both exact), each in one two-term bf16 dot
+// product with (-1, 0) or (0, -1). Those two sit in registers: as literals the
+// compiler encodes the first like the second.
+__device__ __forceinline__ uint32_t pack2_rest(float a, float b, uint32_t hi) {
+  const bf16x2 h = __builtin_bit_cast(bf16x2, hi);
+  uint32_t c0 = 0x0000BF80u, c1 = 0xBF800000u;
+  asm("" : "+v"(c0));
+  asm("" : "+v"(c1));
+  return pack2(__builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2, c0), a, false),
+               __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2, c1), b, false));
+}
 // two accumulator tiles (2s, 2s + 1) as the operand of contraction block s
 __device__ __forceinline__ void make_op(Op8s<bf16>& o, const f32x4& t0, const f32x4& t1) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    o.hi[e] = (bf16)t0[e];
-    o.hi[4 + e] = (bf16)t1[e];
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    o.lo[e] = (bf16)(t0[e] - (float)o.hi[e]);
-    o.lo[4 + e] = (bf16)(t1[e] - (float)o.hi[4 + e]);
-  }
+  uint4 h, l;
+  h.x = pack2(t0[0], t0[1]); h.y = pack2(t0[2], t0[3]);
+  h.z = pack2(t1[0], t1[1]); h.w = pack2(t1[2], t1[3]);
+  l.x = pack2_rest(t0[0], t0[1], h.x); l.y = pack2_rest(t0[2], t0[3], h.y);
+  l.z = pack2_rest(t1[0], t1[1], h.z); l.w = pack2_rest(t1[2], t1[3], h.w);
+  o.hi = __builtin_bit_cast(bf16x8, h);
+  o.lo = __builtin_bit_cast(bf16x8, l);
 }
 __device__ __forceinline__ void make_op(Op8s<float>& o, const f32x4& t0, const f32x4& t1) {
 #pragma unroll
@@ -198,8 +242,7 @@ __device__ __forceinline__ uint2 quad_transpose(uint2 r) {
   return (lane & 2) ? make_uint2(u1, a1) : make_uint2(a0, u0);
 }
 __device__ __forceinline__ uint2 pack4(const f32x4& x) {
-  const bf16x4 h = {(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
-  return __builtin_bit_cast(uint2, h);
+  return make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
 }
 __device__ __forceinline__ f32x4 unpack4(uint2 r) {
   return f32x4{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u),
@@ -209,7 +252,9 @@ __device__ __forceinline__ f32x4 unpack4(uint2 r) {
 // A 16 x 16 tile between row-major memory and the accumulator layout. `row4`
 // is the lane's first row (perm_row4), rows row4 .. row4 + 3, column col0 + l16;
 // element (r, c) at p + r * stride + c, rows >= rows absent (zero / not
-// written). bf16: p 8-byte aligned, stride and col0 multiples of 4.
+// written). bf16: p 8-byte aligned, stride and col0 multiples of 4. p is uniform
+// in the wave and 64 rows span less than 2^31 bytes (checked by the entry
+// points), so a lane's address is a scalar base and a 32-bit offset.
 template <typename T>
 struct TileRaw;
 template <>
@@ -220,17 +265,17 @@ template <>
 struct TileRaw<float> {
   f32x4 r;
 };
-__device__ __forceinline__ void tile_ld(TileRaw<bf16>& t, const bf16* p, int64_t stride, int row4,
+__device__ __forceinline__ void tile_ld(TileRaw<bf16>& t, const bf16* p, uint32_t stride, int row4,
                                         int col0, int rows) {
   const int l16 = threadIdx.x & 15, row = row4 + (l16 & 3);
   t.r = make_uint2(0, 0);
-  if (row < rows) t.r = *reinterpret_cast<const uint2*>(p + row * stride + col0 + 4 * (l16 >> 2));
+  if (row < rows) t.r = *reinterpret_cast<const uint2*>(p + (row * stride + col0 + 4 * (l16 >> 2)));
 }
-__device__ __forceinline__ void tile_ld(TileRaw<float>& t, const float* p, int64_t stride, int row4,
+__device__ __forceinline__ void tile_ld(TileRaw<float>& t, const float* p, uint32_t stride, int row4,
                                         int col0, int rows) {
   const int l16 = threadIdx.x & 15;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) t.r[e] = row4 + e < rows ? p[(row4 + e) * stride + col0 + l16] : 0.f;
+  for (int e = 0; e < 4; ++e) t.r[e] = row4 + e < rows ? p[(uint32_t)((row4 + e) * stride + col0 + l16)] : 0.f;
 }
 __device__ __forceinline__ f32x4 tile_get(const TileRaw<bf16>& t) { return unpack4(quad_transpose(t.r)); }
 __device__ __forceinline__ f32x4 tile_get(const TileRaw<float>& t) { return t.r; }
@@ -242,16 +287,16 @@ __device__ __forceinline__ void tile_op(Op8<bf16>& o, const TileRaw<bf16>& t0, c
 __device__ __forceinline__ void tile_op(Op8<float>& o, const TileRaw<float>& t0, const TileRaw<float>& t1) {
   make_op(o, t0.r, t1.r);
 }
-__device__ __forceinline__ void tile_st(bf16* p, int64_t stride, int row4, int col0, int rows, const f32x4& x) {
+__device__ __forceinline__ void tile_st(bf16* p, uint32_t stride, int row4, int col0, int rows, const f32x4& x) {
   const int l16 = threadIdx.x & 15, row = row4 + (l16 & 3);
   const uint2 r = quad_transpose(pack4(x));
-  if (row < rows) *reinterpret_cast<uint2*>(p + row * stride + col0 + 4 * (l16 >> 2)) = r;
+  if (row < rows) *reinterpret_cast<uint2*>(p + (row * stride + col0 + 4 * (l16 >> 2))) = r;
 }
-__device__ __forceinline__ void tile_st(float* p, int64_t stride, int row4, int col0, int rows, const f32x4& x) {
+__device__ __forceinline__ void tile_st(float* p, uint32_t stride, int row4, int col0, int rows, const f32x4& x) {
   const int l16 = threadIdx.x & 15;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (row4 + e < rows) p[(row4 + e) * stride + col0 + l16] = x[e];
+    if (row4 + e < rows) p[(uint32_t)((row4 + e) * stride + col0 + l16)] = x[e];
 }
 
 // sum over the 16 lanes that hold one accumulator row (rotations inside the
@@ -334,39 +379,63 @@ struct TokTile {
 };
 
 // ------------------------------------------------------------------ global memory -> LDS
-// One wave's 1 KB: lane i's 16 bytes at `src` go to dst + 16 i (dst uniform in
-// the wave) without passing through registers. Complete after lds_dma_wait().
-__device__ __forceinline__ void lds_dma(const void* src, char* dst) {
-  typedef __attribute__((address_space(1))) const void gvoid;
-  typedef __attribute__((address_space(3))) void lvoid;
-  __builtin_amdgcn_global_load_lds((gvoid*)src, (lvoid*)dst, 16, 0, 0);
+// One wave's 1 KB: lane i's 16 bytes at base + off go to LDS byte address
+// dst + 16 i (base and dst uniform in the wave) without passing through
+// registers. Complete after lds_dma_wait() (and, for other waves, a barrier
+// behind it). Written out rather than through the builtin because the
+// compiler, which cannot tell the two buffers apart, waits for every such
+// transfer before the next LDS read of any kind: the prefetch of a chunk would
+// end where the chunk before it begins to read. The instruction writes no
+// register.
+__device__ __forceinline__ void lds_dma(const void* base, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(dst)
+               : "memory", "m0");
 }
 __device__ __forceinline__ void lds_dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// token tile of chunk rows p + r * stride (elements), r < L; rows past L repeat
-// row L - 1 (their factors are zero)
-template <typename T, int K, int NW>
-__device__ __forceinline__ void dma_tok_tile(char* dst, const T* p, int64_t stride, int L, int wave) {
-  using TT = TokTile<T, K>;
-  static_assert(TT::kUnits % (64 * NW) == 0, "whole waves");
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int n = 0; n < TT::kUnits / (64 * NW); ++n) {
-    const int i = n * NW + wave;
-    const int u = 64 * i + lane, r = u / TT::kBlocks, b = (u % TT::kBlocks) ^ TT::swz(r);
-    lds_dma(reinterpret_cast<const char*>(p + min(r, L - 1) * stride) + 16 * b, dst + 1024 * i);
-  }
+// byte address within LDS of a __shared__ object
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  typedef __attribute__((address_space(3))) const char lchar;
+  return (uint32_t)(uintptr_t)(lchar*)p;
 }
-// `bytes` (a multiple of 1 KB) of contiguous memory
+
+// A wave's share of the transfer of token tiles (chunk rows base + r * stride
+// bytes): its 16-byte units' offsets, the same for every full chunk.
+template <typename T, int K, int NW>
+struct TokDma {
+  using TT = TokTile<T, K>;
+  static constexpr int kPer = TT::kUnits / (64 * NW);
+  static_assert(TT::kUnits % (64 * NW) == 0, "whole waves");
+  uint32_t off[kPer], stride;
+  int wave;
+  // rows past `last` repeat it (their factors are zero)
+  __device__ __forceinline__ uint32_t unit(int n, int last) const {
+    const int u = 64 * (n * NW + wave) + (threadIdx.x & 63), r = u / TT::kBlocks;
+    return min(r, last) * stride + 16 * ((u % TT::kBlocks) ^ TT::swz(r));
+  }
+  __device__ __forceinline__ TokDma(uint32_t stride_bytes, int w) : stride(stride_bytes), wave(w) {
+#pragma unroll
+    for (int n = 0; n < kPer; ++n) off[n] = unit(n, kC - 1);
+  }
+  __device__ __forceinline__ void go(uint32_t dst, const T* base, int L) const {
+    if (L >= kC) {
+#pragma unroll
+      for (int n = 0; n < kPer; ++n) lds_dma(base, off[n], dst + 1024 * (n * NW + wave));
+    } else {
+#pragma unroll
+      for (int n = 0; n < kPer; ++n) lds_dma(base, unit(n, L - 1), dst + 1024 * (n * NW + wave));
+    }
+  }
+};
+// `BYTES` (a multiple of 1 KB) of contiguous memory
 template <int BYTES, int NW>
-__device__ __forceinline__ void dma_flat(char* dst, const void* src, int wave) {
+__device__ __forceinline__ void dma_flat(uint32_t dst, const void* src, int wave) {
   static_assert(BYTES % 1024 == 0, "whole waves");
-  const int lane = threadIdx.x & 63;
+  const uint32_t lane = threadIdx.x & 63;
 #pragma unroll
   for (int n = 0; n < (BYTES / 1024 + NW - 1) / NW; ++n) {
     const int i = n * NW + wave;
     if (i >= BYTES / 1024) break;
-    lds_dma(reinterpret_cast<const char*>(src) + 1024 * i + 16 * lane, dst + 1024 * i);
+    lds_dma(reinterpret_cast<const char*>(src) + 1024 * i, 16 * lane, dst + 1024 * i);
   }
 }
 

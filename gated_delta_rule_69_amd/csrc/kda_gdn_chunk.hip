@@ -5,9 +5,9 @@
 //                     head): q k^T and k k^T once on the matrix cores for the
 //                     whole group, then per value head the gate, the FP32
 //                     solve for M, and M, P and the row factors written out.
-//   gdn_scan_kernel   one wave per 16 columns of one (sequence, value head)
-//                     state, walking the chunks in order; S stays in the
-//                     wave's accumulators.
+//   gdn_scan_kernel   16 columns of one (sequence, value head) state per wave,
+//                     walking the chunks in order; S stays in the wave's
+//                     accumulators (gdn_scan32_kernel for FP32 inputs).
 #include "kda_gdn.h"
 
 namespace kda {
@@ -261,158 +261,188 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
 }
 
 // ------------------------------------------------------------------ scan
-// One wave owns 16 columns of S for the whole sequence: K / 16 accumulator
-// tiles. Every product of a chunk step takes an accumulator result of the same
-// wave as its right operand, so the recurrence crosses no barrier and no LDS;
-// LDS only carries the left operands (k, q, M, P, shared by the NW waves),
-// fetched a chunk ahead where two buffers fit. The one barrier per chunk
-// orders those buffers.
-template <typename T, int K, bool BWD>
+// What one workgroup of a scan works on: a chain (sequence, value head) and a
+// block of columns. 1-D grid in groups of 8 chains x NVB column blocks: the
+// blocks of a chain are 8 apart, so they run on one XCD and share its L2 for
+// k, q, M and P. Packed batches take their sequences longest first.
+struct GdnChain {
+  int ok, n, hv, h, vb, len;
+  int64_t bos, c0;  // first token; first chunk
+};
+__device__ __forceinline__ GdnChain gdn_chain(int nvb, const int32_t* cu, const int* table, int N, int T_,
+                                              int H, int HV) {
+  GdnChain r;
+  const int grp = blockIdx.x / (8 * nvb), in = blockIdx.x % (8 * nvb);
+  const int64_t chain = (int64_t)grp * 8 + in % 8;
+  r.ok = chain < (int64_t)N * HV;
+  if (!r.ok) return r;
+  r.n = cu ? table[2 + N + (int)(chain / HV)] : (int)(chain / HV);
+  r.hv = (int)(chain % HV);
+  r.h = r.hv / (HV / H);
+  r.vb = in / 8;
+  seq_range(cu, r.n, T_, &r.bos, &r.len);
+  r.c0 = cu ? table[1 + r.n] : (int64_t)r.n * ((T_ + kC - 1) / kC);
+  return r;
+}
+// empty slot: bitwise passthrough of the state (or +0.0 without one), columns col0 .. + 15
+__device__ __forceinline__ void gdn_pass(const float* h0, float* ht, size_t st, int K, int V, int col0) {
+  for (int e = threadIdx.x & 63; e < K * 16; e += 64) {
+    const size_t off = st + (size_t)(e >> 4) * V + col0 + (e & 15);
+    reinterpret_cast<uint32_t*>(ht)[off] = h0 ? reinterpret_cast<const uint32_t*>(h0)[off] : 0u;
+  }
+}
+
+// bf16. Two waves per 16 columns. The state wave keeps S (K / 16 accumulator
+// tiles) and walks the recurrence: every product of a chunk takes an
+// accumulator result of the wave itself as its right operand, so the
+// recurrence crosses no LDS. The output wave follows one chunk behind: it takes
+// the chunk's start state (already split for the products) and Y through LDS
+// and forms O, and it issues all transfers of left operands (k, q, M, P) into
+// LDS a chunk ahead. With one wave per 16 columns doing both, a chunk step was
+// about 1000 instructions of one wave with nothing else on its SIMD (2.5 us of
+// 3.9 us per chunk at 64 chains); the two halves of the work now run on two.
+// Two barriers per chunk: at its top (operands in LDS) and after the output
+// wave has taken the previous chunk's S and Y.
+//
+// BWD: the backward's run over the forward. S0 and Y are kept instead of O, and
+// dO comes in: o' is formed in full precision (S0 and P split as well; P is
+// strictly lower) for the tokens' scalars of the gate's gradient.
+template <int K, int NP, bool BWD>
 struct GdnScanLds {
-  static constexpr size_t tok = TokTile<T, K>::bytes;
-  static constexpr size_t tri = (BWD ? GdnWs<T>::bwd : GdnWs<T>::fwd) * sizeof(T);
-  static constexpr size_t oQ = tok;
-  static constexpr size_t oM = 2 * tok;       // M, P
-  static constexpr size_t oS = oM + tri;      // row factors: 0..3, or for BWD 0..7
+  static constexpr int NK = K / 32, PT = BWD ? 2 : 1;
+  static constexpr uint32_t tok = TokTile<bf16, K>::bytes, tri = kTriElems * sizeof(bf16);
   static constexpr int scal = (BWD ? 8 : 4) * kC * (int)sizeof(float);
-  static constexpr size_t buf = oS + scal;
-  static constexpr int nbuf = sizeof(T) == 2 ? 2 : 1;
-  static constexpr size_t total = nbuf * buf;
+  // state wave's buffer: k, M (hi, lo), row factors; output wave's: q, P, row factors
+  static constexpr uint32_t sM = tok, sF = sM + 2 * tri, sbuf = sF + scal;
+  static constexpr uint32_t oP = tok, oF = oP + PT * tri, obuf = oF + scal;
+  static constexpr uint32_t at_o = 2 * sbuf, at_x = at_o + 2 * obuf;
+  // exchange of a pair: S0 (BWD: hi, lo), Y, BWD: v - Y
+  static constexpr uint32_t xS = PT * NK * 1024, xY = 4 * 1024, xbuf = xS + (BWD ? 2 : 1) * xY;
+  static constexpr uint32_t total = at_x + NP * xbuf;
 };
 
-// BWD: the backward's run over the forward. S0 and Y are kept; no output, but
-// (bf16) dO comes in and o' is formed in full precision, both its products
-// split, for the tokens' scalars of the gate's gradient (P is strictly lower).
-template <typename T, int K, int V, int NW, bool BWD>
-__global__ void __launch_bounds__(NW * 64)
-gdn_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+template <int K, int V, int NP, bool BWD>
+__global__ void __launch_bounds__(NP * 128)
+gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
                 const float* h0, const int32_t* __restrict__ cu, const int* __restrict__ table, int N,
-                int T_, int H, int HV, const float* __restrict__ ws_scal,
-                const T* __restrict__ ws_frag, int write_final, T* __restrict__ o, float* ht,
-                const T* __restrict__ dO, const float* __restrict__ dht, T* __restrict__ ws_S0,
-                T* __restrict__ ws_Y, float* __restrict__ ws_tok, float* __restrict__ ws_end) {
+                int T_, int H, int HV, const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag,
+                int write_final, bf16* __restrict__ o, float* ht, const bf16* __restrict__ dO,
+                const float* __restrict__ dht, bf16* __restrict__ ws_S0, bf16* __restrict__ ws_Y,
+                float* __restrict__ ws_tok, float* __restrict__ ws_end) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  using Lds = GdnScanLds<T, K, BWD>;
-  using TT = TokTile<T, K>;
-  constexpr int NK = K / 32, RT = K / 16, BV = 16 * NW, NVB = V / BV, PT = GdnWs<T>::kParts;
-  constexpr bool kOut = !BWD || GdnWs<T>::kScanGate;  // o is formed
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // 1-D grid in groups of 8 chains x NVB column blocks: the blocks of a chain
-  // are 8 apart, so they run on one XCD and share its L2 for k, q, M and P
-  const int grp = blockIdx.x / (8 * NVB), in = blockIdx.x % (8 * NVB);
-  const int64_t chain = (int64_t)grp * 8 + in % 8;
-  if (chain >= (int64_t)N * HV) return;
-  const int n = cu ? table[2 + N + (int)(chain / HV)] : (int)(chain / HV);
-  const int hv = (int)(chain % HV), h = hv / (HV / H);
-  const int col0 = (in / 8) * BV + 16 * wave;
-  int64_t bos;
-  int len;
-  seq_range(cu, n, T_, &bos, &len);
-  const size_t st = ((size_t)n * HV + hv) * (size_t)K * V;
+  using L_ = GdnScanLds<K, NP, BWD>;
+  using TT = TokTile<bf16, K>;
+  constexpr int NK = K / 32, RT = K / 16, BV = 16 * NP, NVB = V / BV;
+  constexpr size_t kFrag = BWD ? GdnWs<bf16>::bwd : GdnWs<bf16>::fwd;
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pair = wave % NP;
+  const bool state_wave = wave < NP;
+  const GdnChain ch = gdn_chain(NVB, cu, table, N, T_, H, HV);
+  if (!ch.ok) return;
+  const int col0 = ch.vb * BV + 16 * pair, hv = ch.hv, len = ch.len;
+  const size_t st = ((size_t)ch.n * HV + hv) * (size_t)K * V;
   if (len <= 0) {
-    // empty slot: bitwise passthrough of the state (or +0.0 without one)
-    if constexpr (BWD) return;
-    if (!write_final || (h0 == ht && h0 != nullptr)) return;
-    for (int e = lane; e < K * 16; e += 64) {
-      const size_t off = st + (size_t)(e >> 4) * V + col0 + (e & 15);
-      reinterpret_cast<uint32_t*>(ht)[off] = h0 ? reinterpret_cast<const uint32_t*>(h0)[off] : 0u;
-    }
+    if (!BWD && state_wave && write_final && !(h0 == ht && h0 != nullptr)) gdn_pass(h0, ht, st, K, V, col0);
     return;
   }
   const int nc = (len + kC - 1) / kC;
-  const int64_t c0 = cu ? table[1 + n] : (int64_t)n * ((T_ + kC - 1) / kC);
+  auto chunk = [&](int c) { return (size_t)(ch.c0 + c) * HV + hv; };
+  auto tokens = [&](int c) { return min(kC, len - c * kC); };
+  auto vrow = [&](int c) { return ((ch.bos + (int64_t)c * kC) * HV + hv) * V; };
+  char* xch = smem + L_::at_x + pair * L_::xbuf;
 
-  auto fetch = [&](int c, char* b) {
-    const size_t ch = (size_t)(c0 + c) * HV + hv;
-    const int64_t row = ((bos + (int64_t)c * kC) * H + h) * K;
-    const int L = min(kC, len - c * kC);
-    dma_tok_tile<T, K, NW>(b, k + row, (int64_t)H * K, L, wave);
-    dma_tok_tile<T, K, NW>(b + Lds::oQ, q + row, (int64_t)H * K, L, wave);
-    dma_flat<(int)Lds::tri, NW>(b + Lds::oM, ws_frag + ch * (Lds::tri / sizeof(T)), wave);
-    dma_flat<Lds::scal, NW>(b + Lds::oS, ws_scal + ch * (kGdnScal * kC), wave);
-  };
-  TileRaw<T> vr[4], dr[4];
-  float gl;
-  auto fetch_v = [&](int c) {
-    const int L = min(kC, len - c * kC);
-    const int64_t at = ((bos + (int64_t)c * kC) * HV + hv) * V;
+  if (state_wave) {
+    f32x4 S[RT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      tile_ld(vr[t], v + at, (int64_t)HV * V, perm_row4(t, g), col0, L);
-      if constexpr (BWD && GdnWs<T>::kScanGate)
-        tile_ld(dr[t], dO + at, (int64_t)HV * V, perm_row4(t, g), col0, L);
-    }
-    gl = ws_scal[((size_t)(c0 + c) * HV + hv) * (kGdnScal * kC) + kSl * kC];
-  };
-
-  f32x4 S[RT];
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+      for (int e = 0; e < 4; ++e)
+        S[r][e] = h0 ? h0[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] : 0.f;
+    TileRaw<bf16> vr[4];
+    float gl;
+    auto fetch_v = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      S[r][e] = h0 ? h0[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] : 0.f;
-
-  fetch(0, smem);
-  fetch_v(0);
-  for (int c = 0; c < nc; ++c) {
-    const char* b = smem + (Lds::nbuf == 2 ? (c & 1) * Lds::buf : 0);
-    lds_dma_wait();
-    __syncthreads();  // this chunk's operands are in LDS; the other buffer is no longer read
-    if (Lds::nbuf == 2 && c + 1 < nc) fetch(c + 1, smem + ((c + 1) & 1) * Lds::buf);
-    const float* sf = reinterpret_cast<const float*>(b + Lds::oS);
-    const T* sM = reinterpret_cast<const T*>(b + Lds::oM);
-    const T* sP = sM + PT * kTriElems;
-    const size_t ch = (size_t)(c0 + c) * HV + hv;
-    const int L = min(kC, len - c * kC);
-    f32x4 x[4], dot[4];
+      for (int t = 0; t < 4; ++t) tile_ld(vr[t], v + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
+      gl = ws_scal[chunk(c) * (kGdnScal * kC) + kSl * kC];
+    };
+    fetch_v(0);
+    __syncthreads();  // the first chunk's operands
+    for (int it = 0; it <= nc; ++it) {
+      __syncthreads();
+      if (it == nc) {
+        __syncthreads();
+        break;
+      }
+      const char* b = smem + (it & 1) * L_::sbuf;
+      const bf16* sM = reinterpret_cast<const bf16*>(b + L_::sM);
+      const float* sf = reinterpret_cast<const float*>(b + L_::sF);
+      // Left operands are read from LDS a group ahead of the products that take
+      // them (`stage` keeps the compiler from moving the reads back to their use).
+      Op8<bf16> ka[NK][4];
+      auto read_k = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      x[t] = tile_get(vr[t]);
-      if constexpr (BWD && GdnWs<T>::kScanGate) dot[t] = tile_get(dr[t]);
-    }
-    const float el = gl;
-    if (c + 1 < nc) fetch_v(c + 1);
-
-    if constexpr (BWD) {
+        for (int t = 0; t < 4; ++t) TT::rows(ka[s][t], b, t, s);
+      };
+      read_k(0);
+      read_k(1);
+      f32x4 x[4];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) tile_st(ws_S0 + ch * K * V, V, perm_row4(r, g), col0, K, S[r]);
-    }
-    // k S0 (split: it feeds the state) and q S0
-    f32x4 ks[4], qs[4];
+      for (int t = 0; t < 4; ++t) x[t] = tile_get(vr[t]);
+      const float el = gl;
+      if (it + 1 < nc) fetch_v(it + 1);
+      // k S0, both parts of S0: it feeds the state
+      Op8s<bf16> sb[NK];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) ks[t] = qs[t] = zero4();
+      for (int s = 0; s < NK; ++s) make_op(sb[s], S[2 * s], S[2 * s + 1]);
+      f32x4 ks[4];
 #pragma unroll
-    for (int s = 0; s < NK; ++s) {
-      Op8s<T> sb;
-      make_op(sb, S[2 * s], S[2 * s + 1]);
+      for (int t = 0; t < 4; ++t) ks[t] = zero4();
+      Op8<bf16> ml[2][6];
+      auto read_m = [&](int f) __attribute__((always_inline)) {
+        ld_op(ml[0][f], sM + f * kFragElems + lane * 8);
+        ld_op(ml[1][f], sM + kTriElems + f * kFragElems + lane * 8);
+      };
+#pragma unroll
+      for (int s = 0; s < NK; ++s) {
+        stage();
+        if (s + 2 < NK) {
+          read_k(s + 2);
+        } else {
+          read_m(2 * (s + 2 - NK));
+          read_m(2 * (s + 2 - NK) + 1);
+        }
+        stage();
+        mma_rows(ka[s], sb[s], ks);
+      }
+      stage();
+      read_m(4);
+      read_m(5);
+      __syncthreads();  // the output wave has taken the previous chunk's S0 and Y
+#pragma unroll
+      for (int s = 0; s < NK; ++s) {
+        *reinterpret_cast<bf16x8*>(xch + (s * 64 + lane) * 16) = sb[s].hi;
+        if constexpr (BWD) *reinterpret_cast<bf16x8*>(xch + ((NK + s) * 64 + lane) * 16) = sb[s].lo;
+      }
+      // R = v - e^G k S0, then Y = R - M (b R)
+      f32x4 bb[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        Op8<T> a;
-        TT::rows(a, b, t, s);
-        ks[t] = mma8s(a, sb, ks[t]);
-        if constexpr (kOut) {
-          TT::rows(a, b + Lds::oQ, t, s);
-          qs[t] = BWD ? mma8s(a, sb, qs[t]) : mma8h(a, sb, qs[t]);
+        float f[4], w[4];
+        lds4(sf + kSk * kC + perm_row4(t, g), f);
+        lds4(sf + kSb * kC + perm_row4(t, g), w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (BWD) {
+            ks[t][e] *= f[e];
+            x[t][e] -= ks[t][e];
+          } else {
+            x[t][e] = fmaf(-f[e], ks[t][e], x[t][e]);
+          }
+          bb[t][e] = w[e];
         }
       }
-    }
-    // R = v - e^G k S0, then Y = R - M (b R)
-    f32x4 bb[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      float f[4], w[4];
-      lds4(sf + kSk * kC + perm_row4(t, g), f);
-      lds4(sf + kSb * kC + perm_row4(t, g), w);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        ks[t][e] *= f[e];
-        x[t][e] -= ks[t][e];
-        bb[t][e] = w[e];
-      }
-    }
-    {
-      Op8s<T> rb[2];
+      Op8s<bf16> rb[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         f32x4 a0, a1;
@@ -423,32 +453,342 @@ gdn_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __res
         }
         make_op(rb[s], a0, a1);
       }
+      if constexpr (BWD) {
+        f32x4 m[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        f32x4 m = zero4();
+        for (int t = 0; t < 4; ++t) m[t] = zero4();
+        mma_tri<2>(ml, rb, m);
 #pragma unroll
-        for (int s = 0; s <= (t >> 1); ++s) {
-          Op8<T> a;
-          if constexpr (sizeof(T) == 2) {
-            ld_op(a, sM + kTriElems + frag_low(t, s) * kFragElems + lane * 8);
-            m = mma8h(a, rb[s], m);
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[t][e] += m[t][e];
+            ks[t][e] -= m[t][e];  // v - Y, without v
           }
-          ld_op(a, sM + frag_low(t, s) * kFragElems + lane * 8);
-          m = mma8s(a, rb[s], m);
+          *reinterpret_cast<f32x4*>(xch + L_::xS + L_::xY + (t * 64 + lane) * 16) = ks[t];
         }
+      } else {
+        mma_tri<2>(ml, rb, x);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(xch + L_::xS + (t * 64 + lane) * 16) = x[t];
+      // S1 = e^{G_last} S0 + K^T (e^{G_last - G} b Y)
+      Op8<bf16> kc[RT][2];
+      auto read_kc = [&](int r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) TT::cols(kc[r][s], b, r, s);
+      };
+      read_kc(0);
+      read_kc(1);
+      Op8s<bf16> eb[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        f32x4 ed[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = 2 * s + i;
+          float f[4];
+          lds4(sf + kSe * kC + perm_row4(t, g), f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ed[i][e] = f[e] * (bb[t][e] * x[t][e]);
+        }
+        make_op(eb[s], ed[0], ed[1]);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; r += 2) {
+        stage();
+        if (r + 2 < RT) {
+          read_kc(r + 2);
+          read_kc(r + 3);
+        }
+        stage();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[t][e] += m[e];
-          ks[t][e] -= m[e];  // v - Y, without v
+          S[r][e] *= el;
+          S[r + 1][e] *= el;
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          S[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r][s].v, eb[s].lo, S[r], 0, 0, 0);
+          S[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r + 1][s].v, eb[s].lo, S[r + 1], 0, 0, 0);
+          S[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r][s].v, eb[s].hi, S[r], 0, 0, 0);
+          S[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r + 1][s].v, eb[s].hi, S[r + 1], 0, 0, 0);
         }
       }
     }
     if constexpr (BWD) {
+      if (dht) {
+        float y = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) tile_st(ws_Y + ch * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y = fmaf(S[r][e], dht[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16], y);
+        y = row16_sum(y);
+        y += __shfl_xor(y, 16);
+        y += __shfl_xor(y, 32);
+        if (lane == 0) ws_end[((size_t)ch.n * HV + hv) * (V / 16) + (col0 >> 4)] = y;
+      }
+    } else if (write_final) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          ht[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] = S[r][e];
     }
-    // Delta = b Y; O = e^G q~ S0 + P Delta
-    Op8s<T> eb[2];
+    return;
+  }
+
+  // ---- output wave
+  const uint32_t lds = lds_addr(smem);
+  const TokDma<bf16, K, NP> tok((uint32_t)(H * K * sizeof(bf16)), pair);
+  auto fetch_s = [&](int c) __attribute__((always_inline)) {  // what the state waves read
+    const uint32_t b = lds + (c & 1) * L_::sbuf;
+    tok.go(b, k + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
+    dma_flat<2 * L_::tri, NP>(b + L_::sM, ws_frag + chunk(c) * kFrag, pair);
+    dma_flat<L_::scal, NP>(b + L_::sF, ws_scal + chunk(c) * (kGdnScal * kC), pair);
+  };
+  auto fetch_o = [&](int c) __attribute__((always_inline)) {  // what the output waves read
+    const uint32_t b = lds + L_::at_o + (c & 1) * L_::obuf;
+    tok.go(b, q + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
+    dma_flat<L_::PT * L_::tri, NP>(b + L_::oP, ws_frag + chunk(c) * kFrag + 2 * kTriElems, pair);
+    dma_flat<L_::scal, NP>(b + L_::oF, ws_scal + chunk(c) * (kGdnScal * kC), pair);
+  };
+  TileRaw<bf16> dr[4];
+  fetch_s(0);
+  lds_dma_wait();
+  __syncthreads();
+  for (int it = 0; it <= nc; ++it) {
+    lds_dma_wait();
+    __syncthreads();
+    if (it + 1 < nc) fetch_s(it + 1);
+    if (it < nc) fetch_o(it);
+    const int c = it - 1;
+    Op8s<bf16> sb[NK];
+    f32x4 x[4], pred[4], dot[4];
+    if (it > 0) {
+#pragma unroll
+      for (int s = 0; s < NK; ++s) {
+        sb[s].hi = *reinterpret_cast<const bf16x8*>(xch + (s * 64 + lane) * 16);
+        if constexpr (BWD) sb[s].lo = *reinterpret_cast<const bf16x8*>(xch + ((NK + s) * 64 + lane) * 16);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        x[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + (t * 64 + lane) * 16);
+        if constexpr (BWD) pred[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + L_::xY + (t * 64 + lane) * 16);
+      }
+    }
+    __syncthreads();
+    if (it == 0) {
+      if constexpr (BWD) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) tile_ld(dr[t], dO + vrow(0), HV * V, perm_row4(t, g), col0, tokens(0));
+      }
+      continue;
+    }
+    const char* b = smem + L_::at_o + (c & 1) * L_::obuf;
+    const bf16* sP = reinterpret_cast<const bf16*>(b + L_::oP);
+    const float* sf = reinterpret_cast<const float*>(b + L_::oF);
+    if constexpr (BWD) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) dot[t] = tile_get(dr[t]);
+      if (it < nc) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) tile_ld(dr[t], dO + vrow(it), HV * V, perm_row4(t, g), col0, tokens(it));
+      }
+      // S0 (its high part) row by row, and Y
+      bf16* s0 = ws_S0 + chunk(c) * K * V;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const uint4 w = __builtin_bit_cast(uint4, sb[r >> 1].hi);
+        const uint2 y = quad_transpose((r & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y));
+        *reinterpret_cast<uint2*>(s0 + (uint32_t)((perm_row4(r, g) + (l16 & 3)) * V + col0 + 4 * (l16 >> 2))) = y;
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) tile_st(ws_Y + chunk(c) * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+    }
+    // O = e^G q~ S0 + P Delta, Delta = b Y
+    Op8<bf16> qa[2][4], pf[L_::PT][6];
+    f32x4 qs[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) qs[t] = zero4();
+    auto read_q = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) TT::rows(qa[s & 1][t], b, t, s);
+    };
+    read_q(0);
+    float bb[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) lds4(sf + kSb * kC + perm_row4(t, g), bb[t]);
+    Op8s<bf16> db[2];  // split: with S0 and P rounded as well, hi alone left o at 1.65x its rounding error
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      f32x4 d[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[i][e] = bb[2 * s + i][e] * x[2 * s + i][e];
+      make_op(db[s], d[0], d[1]);
+    }
+#pragma unroll
+    for (int s = 0; s < NK; ++s) {
+      stage();
+      if (s + 1 < NK) {
+        read_q(s + 1);
+      } else {
+#pragma unroll
+        for (int pt = 0; pt < L_::PT; ++pt)
+#pragma unroll
+          for (int f = 0; f < 6; ++f) ld_op(pf[pt][f], sP + pt * kTriElems + f * kFragElems + lane * 8);
+      }
+      stage();
+      if constexpr (BWD) {
+        mma_rows(qa[s & 1], sb[s], qs);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) qs[t] = mma8h(qa[s & 1][t], sb[s], qs[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float f[4];
+      lds4(sf + kSq * kC + perm_row4(t, g), f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qs[t][e] *= f[e];
+    }
+    mma_tri<L_::PT>(pf, db, qs);
+    if constexpr (BWD) {
+      float* tk = ws_tok + (chunk(c) * (V / 16) + (col0 >> 4)) * kC;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float f[4], y[4];
+        lds4(sf + kSp * kC + perm_row4(t, g), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = row16_sum(dot[t][e] * (qs[t][e] - f[e] * bb[t][e] * pred[t][e]));
+        if (l16 == 0) *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = make_float4(y[0], y[1], y[2], y[3]);
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) tile_st(o + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c), qs[t]);
+    }
+  }
+}
+
+// FP32. The same step by one wave per 16 columns, on the FP32 matrix cores;
+// operands need no splitting. One operand buffer (two do not fit). BWD keeps
+// S0 and Y and forms no output.
+template <int K, bool BWD>
+struct GdnScan32Lds {
+  static constexpr uint32_t tok = TokTile<float, K>::bytes, tri = kTriElems * sizeof(float);
+  static constexpr uint32_t oQ = tok, oM = 2 * tok, oS = oM + 2 * tri, total = oS + 4 * kC * sizeof(float);
+};
+
+template <int K, int V, int NW, bool BWD>
+__global__ void __launch_bounds__(NW * 64)
+gdn_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                  const float* h0, const int32_t* __restrict__ cu, const int* __restrict__ table, int N, int T_,
+                  int H, int HV, const float* __restrict__ ws_scal, const float* __restrict__ ws_frag,
+                  int write_final, float* __restrict__ o, float* ht, float* __restrict__ ws_S0,
+                  float* __restrict__ ws_Y) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  using L_ = GdnScan32Lds<K, BWD>;
+  using TT = TokTile<float, K>;
+  constexpr int NK = K / 32, RT = K / 16, BV = 16 * NW, NVB = V / BV;
+  constexpr size_t kFrag = GdnWs<float>::fwd;
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const GdnChain ch = gdn_chain(NVB, cu, table, N, T_, H, HV);
+  if (!ch.ok) return;
+  const int col0 = ch.vb * BV + 16 * wave, hv = ch.hv, len = ch.len;
+  const size_t st = ((size_t)ch.n * HV + hv) * (size_t)K * V;
+  if (len <= 0) {
+    if (!BWD && write_final && !(h0 == ht && h0 != nullptr)) gdn_pass(h0, ht, st, K, V, col0);
+    return;
+  }
+  const int nc = (len + kC - 1) / kC;
+  const uint32_t lds = lds_addr(smem);
+  const TokDma<float, K, NW> tok((uint32_t)(H * K * sizeof(float)), wave);
+  auto fetch = [&](int c) {
+    const size_t cc = (size_t)(ch.c0 + c) * HV + hv;
+    const int64_t row = ((ch.bos + (int64_t)c * kC) * H + ch.h) * K;
+    const int L = min(kC, len - c * kC);
+    tok.go(lds, k + row, L);
+    if constexpr (!BWD) tok.go(lds + L_::oQ, q + row, L);
+    dma_flat<2 * L_::tri, NW>(lds + L_::oM, ws_frag + cc * kFrag, wave);
+    dma_flat<4 * kC * 4, NW>(lds + L_::oS, ws_scal + cc * (kGdnScal * kC), wave);
+  };
+  f32x4 S[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      S[r][e] = h0 ? h0[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] : 0.f;
+  const float* sf = reinterpret_cast<const float*>(smem + L_::oS);
+  const float* sM = reinterpret_cast<const float*>(smem + L_::oM);
+  const float* sP = sM + kTriElems;
+  for (int c = 0; c < nc; ++c) {
+    if (c > 0) __syncthreads();  // every wave is done with the buffer
+    fetch(c);
+    const size_t cc = (size_t)(ch.c0 + c) * HV + hv;
+    const int L = min(kC, len - c * kC);
+    const int64_t at = ((ch.bos + (int64_t)c * kC) * HV + hv) * V;
+    f32x4 x[4], ks[4], qs[4], bb[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      TileRaw<float> r;
+      tile_ld(r, v + at, HV * V, perm_row4(t, g), col0, L);
+      x[t] = r.r;
+      ks[t] = qs[t] = zero4();
+    }
+    const float el = ws_scal[cc * (kGdnScal * kC) + kSl * kC];
+    if constexpr (BWD) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) tile_st(ws_S0 + cc * K * V, V, perm_row4(r, g), col0, K, S[r]);
+    }
+    lds_dma_wait();
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < NK; ++s) {
+      Op8s<float> sb;
+      make_op(sb, S[2 * s], S[2 * s + 1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        Op8<float> a;
+        TT::rows(a, smem, t, s);
+        ks[t] = mma8s(a, sb, ks[t]);
+        if constexpr (!BWD) {
+          TT::rows(a, smem + L_::oQ, t, s);
+          qs[t] = mma8s(a, sb, qs[t]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      float f[4], w[4];
+      lds4(sf + kSk * kC + perm_row4(t, g), f);
+      lds4(sf + kSb * kC + perm_row4(t, g), w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[t][e] = fmaf(-f[e], ks[t][e], x[t][e]);
+        bb[t][e] = w[e];
+      }
+    }
+    Op8s<float> rb[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) make_op(rb[s], -bb[2 * s] * x[2 * s], -bb[2 * s + 1] * x[2 * s + 1]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int s = 0; s <= (t >> 1); ++s) {
+        Op8<float> a;
+        ld_op(a, sM + frag_low(t, s) * kFragElems + lane * 8);
+        x[t] = mma8s(a, rb[s], x[t]);
+      }
+    if constexpr (BWD) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) tile_st(ws_Y + cc * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+    }
+    Op8s<float> eb[2], db[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       f32x4 d[2], ed[2];
@@ -464,76 +804,37 @@ gdn_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __res
         }
       }
       make_op(eb[s], ed[0], ed[1]);
-      if constexpr (kOut) {
-        Op8s<T> db;  // split: with S0 and P rounded as well, hi alone left o at 1.65x its rounding error
-        make_op(db, d[0], d[1]);
-        if (s == 0) {
-  #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            float f[4];
-            lds4(sf + kSq * kC + perm_row4(t, g), f);
-  #pragma unroll
-            for (int e = 0; e < 4; ++e) qs[t][e] *= f[e];
-          }
-        }
-  #pragma unroll
-        for (int t = 2 * s; t < 4; ++t) {
-          Op8<T> a;
-          if constexpr (BWD && PT == 2) {
-            ld_op(a, sP + kTriElems + frag_low(t, s) * kFragElems + lane * 8);
-            qs[t] = mma8h(a, db, qs[t]);
-          }
+      make_op(db[s], d[0], d[1]);
+    }
+    if constexpr (!BWD) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        float f[4];
+        lds4(sf + kSq * kC + perm_row4(t, g), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qs[t][e] *= f[e];
+#pragma unroll
+        for (int s = 0; s <= (t >> 1); ++s) {
+          Op8<float> a;
           ld_op(a, sP + frag_low(t, s) * kFragElems + lane * 8);
-          qs[t] = mma8s(a, db, qs[t]);
+          qs[t] = mma8s(a, db[s], qs[t]);
         }
+        tile_st(o + at, HV * V, perm_row4(t, g), col0, L, qs[t]);
       }
     }
-    // S1 = e^{G_last} S0 + K^T (e^{G_last - G} Delta)
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[r][e] *= el;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        Op8<T> a;
-        TT::cols(a, b, r, s);
+        Op8<float> a;
+        TT::cols(a, smem, r, s);
         S[r] = mma8s(a, eb[s], S[r]);
       }
     }
-    if constexpr (BWD && GdnWs<T>::kScanGate) {
-      float* tk = ws_tok + (ch * (V / 16) + (col0 >> 4)) * kC;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        float f[4], y[4];
-        lds4(sf + kSp * kC + perm_row4(t, g), f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = row16_sum(dot[t][e] * (qs[t][e] - f[e] * bb[t][e] * ks[t][e]));
-        if (l16 == 0) *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = make_float4(y[0], y[1], y[2], y[3]);
-      }
-    } else if constexpr (!BWD) {
-      T* ob = o + ((bos + (int64_t)c * kC) * HV + hv) * V;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) tile_st(ob, (int64_t)HV * V, perm_row4(t, g), col0, L, qs[t]);
-    }
-    if (Lds::nbuf == 1 && c + 1 < nc) {
-      __syncthreads();  // every wave is done with the only buffer
-      fetch(c + 1, smem);
-    }
   }
-  if constexpr (BWD) {
-    if (GdnWs<T>::kScanGate && dht) {
-      float y = 0.f;
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y = fmaf(S[r][e], dht[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16], y);
-      y = row16_sum(y);
-      y += __shfl_xor(y, 16);
-      y += __shfl_xor(y, 32);
-      if (lane == 0) ws_end[((size_t)n * HV + hv) * (V / 16) + (col0 >> 4)] = y;
-    }
-  } else if (write_final) {
+  if (!BWD && write_final) {
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -560,17 +861,28 @@ struct GdnCall {
   const float* dht;
 };
 
-template <typename T, int K, int V, int NW, bool BWD>
-static hipError_t scan_t(const kda_dims& d, const GdnCall& c, const GdnLayout<T>& w, hipStream_t s) {
-  constexpr size_t lds = GdnScanLds<T, K, BWD>::total;
+// bf16 in NP pairs of waves, FP32 in NP waves: 16 NP columns per workgroup
+template <int K, int V, int NP, bool BWD>
+static hipError_t scan_t(const kda_dims& d, const GdnCall& c, const GdnLayout<bf16>& w, hipStream_t s) {
+  constexpr size_t lds = GdnScanLds<K, NP, BWD>::total;
   static_assert(lds <= 160 * 1024, "LDS");
-  hipError_t e = set_lds(&gdn_scan_kernel<T, K, V, NW, BWD>, lds);
+  hipError_t e = set_lds(&gdn_scan_kernel<K, V, NP, BWD>, lds);
   if (e != hipSuccess) return e;
-  const int64_t chains = (int64_t)d.N * d.HV;
-  hipLaunchKernelGGL((gdn_scan_kernel<T, K, V, NW, BWD>), dim3(scan_grid(chains, V, 16 * NW)), dim3(64 * NW),
-                     lds, s, (const T*)c.q, (const T*)c.k, (const T*)c.v, c.h0, c.cu, w.table, d.N, d.T, d.H,
-                     d.HV, w.scal, w.frag, c.ht != nullptr, (T*)c.o, c.ht, (const T*)c.dO, c.dht, w.S0, w.Y,
-                     w.tok, w.end);
+  hipLaunchKernelGGL((gdn_scan_kernel<K, V, NP, BWD>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
+                     dim3(128 * NP), lds, s, (const bf16*)c.q, (const bf16*)c.k, (const bf16*)c.v, c.h0, c.cu,
+                     w.table, d.N, d.T, d.H, d.HV, w.scal, w.frag, c.ht != nullptr, (bf16*)c.o, c.ht,
+                     (const bf16*)c.dO, c.dht, w.S0, w.Y, w.tok, w.end);
+  return hipGetLastError();
+}
+template <int K, int V, int NP, bool BWD>
+static hipError_t scan_t(const kda_dims& d, const GdnCall& c, const GdnLayout<float>& w, hipStream_t s) {
+  constexpr size_t lds = GdnScan32Lds<K, BWD>::total;
+  static_assert(lds <= 160 * 1024, "LDS");
+  hipError_t e = set_lds(&gdn_scan32_kernel<K, V, NP, BWD>, lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((gdn_scan32_kernel<K, V, NP, BWD>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
+                     dim3(64 * NP), lds, s, (const float*)c.q, (const float*)c.k, (const float*)c.v, c.h0, c.cu,
+                     w.table, d.N, d.T, d.H, d.HV, w.scal, w.frag, c.ht != nullptr, (float*)c.o, c.ht, w.S0, w.Y);
   return hipGetLastError();
 }
 
@@ -595,8 +907,12 @@ static hipError_t gdn_fwd_kv(const kda_dims& d, const GdnCall& c, void* ws, hipS
     if (e != hipSuccess) return e;
   }
   // 64 columns per workgroup while that fills the device, else 32
+  // (the backward's exchange of 64 columns does not fit LDS)
   const bool wide = (int64_t)d.N * d.HV * (V / 64) >= kda_host::device_cus();
-  return wide ? scan_t<T, K, V, 4, BWD>(d, c, w, s) : scan_t<T, K, V, 2, BWD>(d, c, w, s);
+  if constexpr (!BWD || sizeof(T) == 4) {
+    if (wide) return scan_t<K, V, 4, BWD>(d, c, w, s);
+  }
+  return scan_t<K, V, 2, BWD>(d, c, w, s);
 }
 
 template <typename T, bool BWD>

@@ -87,12 +87,14 @@ gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
   const int nc = (len + kC - 1) / kC;
   const int64_t c0 = cu ? table[1 + n] : (int64_t)n * ((T_ + kC - 1) / kC);
 
-  auto fetch = [&](int c, char* b) {
+  const uint32_t lds = lds_addr(smem);
+  const TokDma<T, K, NW> tok((uint32_t)(H * K * sizeof(T)), wave);
+  auto fetch = [&](int c, uint32_t b) {
     const size_t ch = (size_t)(c0 + c) * HV + hv;
     const int64_t row = ((bos + (int64_t)c * kC) * H + h) * K;
     const int L = min(kC, len - c * kC);
-    dma_tok_tile<T, K, NW>(b, k + row, (int64_t)H * K, L, wave);
-    dma_tok_tile<T, K, NW>(b + Lds::oQ, q + row, (int64_t)H * K, L, wave);
+    tok.go(b, k + row, L);
+    tok.go(b + Lds::oQ, q + row, L);
     dma_flat<(int)Lds::tri, NW>(b + Lds::oM, ws_bwd + ch * GdnWs<T>::bwd, wave);
     dma_flat<Lds::scal, NW>(b + Lds::oS, ws_scal + ch * (kGdnScal * kC), wave);
   };
@@ -103,8 +105,8 @@ gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     const int64_t at = ((bos + (int64_t)c * kC) * HV + hv) * V;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      tile_ld(dr[t], dO + at, (int64_t)HV * V, perm_row4(t, g), col0, L);
-      if constexpr (kGate) tile_ld(vr[t], v + at, (int64_t)HV * V, perm_row4(t, g), col0, L);
+      tile_ld(dr[t], dO + at, HV * V, perm_row4(t, g), col0, L);
+      if constexpr (kGate) tile_ld(vr[t], v + at, HV * V, perm_row4(t, g), col0, L);
     }
     if constexpr (kGate) od = ws_tok[(((size_t)(c0 + c) * HV + hv) * (V / 16) + (col0 >> 4)) * kC + lane];
     gl = ws_scal[((size_t)(c0 + c) * HV + hv) * (kGdnScal * kC) + kSl * kC];
@@ -120,7 +122,7 @@ gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
   // sum over the tokens behind this chunk of <o, dO> - <v, dv>, these columns
   double behind = kGate && dht ? (double)ws_end[((size_t)n * HV + hv) * (V / 16) + (col0 >> 4)] : 0.;
   int buf = 0;
-  fetch(nc - 1, smem);
+  fetch(nc - 1, lds);
   fetch_do(nc - 1);
   for (int c = nc - 1; c >= 0; --c) {
     const char* b = smem + buf * Lds::buf;
@@ -128,7 +130,7 @@ gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     __syncthreads();
     if (Lds::nbuf == 2) {
       buf ^= 1;
-      if (c > 0) fetch(c - 1, smem + buf * Lds::buf);
+      if (c > 0) fetch(c - 1, lds + buf * (uint32_t)Lds::buf);
     }
     const float* sf = reinterpret_cast<const float*>(b + Lds::oS);
     const T* sM = reinterpret_cast<const T*>(b + Lds::oM);
@@ -257,7 +259,7 @@ gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     T* vb = dv + ((bos + (int64_t)c * kC) * HV + hv) * V;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      tile_st(vb, (int64_t)HV * V, perm_row4(t, g), col0, L, x[t]);
+      tile_st(vb, HV * V, perm_row4(t, g), col0, L, x[t]);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -287,7 +289,7 @@ gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     }
     if (Lds::nbuf == 1 && c > 0) {
       __syncthreads();
-      fetch(c - 1, smem);
+      fetch(c - 1, lds);
     }
   }
   if (dh0) {
@@ -334,8 +336,10 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
   char* sQ = smem + TT::bytes;
   {
     const int64_t row = (geo.t0 * H + h) * K;
-    dma_tok_tile<T, K, 4>(sK, k + row, (int64_t)H * K, L, wave);
-    dma_tok_tile<T, K, 4>(sQ, q + row, (int64_t)H * K, L, wave);
+    const TokDma<T, K, 4> tok((uint32_t)(H * K * sizeof(T)), wave);
+    const uint32_t lds = lds_addr(smem);
+    tok.go(lds, k + row, L);
+    tok.go(lds + TT::bytes, q + row, L);
   }
   const int own = perm_row(wave, l16);   // this lane's row as an operand
   const int own4 = perm_row4(wave, g);   // first of its four accumulator rows
