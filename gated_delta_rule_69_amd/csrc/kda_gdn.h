@@ -60,18 +60,20 @@ __host__ __device__ constexpr int frag_up(int t, int s) { return t < 2 ? 2 * t +
 constexpr int kFragElems = 64 * 8;          // one fragment: [lane][8]
 constexpr int kTriElems = 6 * kFragElems;   // one triangular matrix
 
-// Row factors of a (chunk, value head), FP32 [kGdnScal][64] (one 16-byte aligned block):
+// Row factors of a (chunk, value head), FP32 [kGdnScal][64], ordered so that what one
+// reader takes is consecutive:
 enum GdnScal : int {
   kSk = 0,   // e^G rk                 (rk, rq: 1, or the inverse L2 norms of k and q rows)
-  kSq = 1,   // e^G rq / sqrt(K)
-  kSe = 2,   // e^{G_last - G} rk
+  kSeb = 1,  // e^{G_last - G} rk b
+  kSl = 2,   // e^{G_last}, 64 times
   kSb = 3,   // b
-  kSl = 4,   // [0] e^{G_last}
-  kSp = 5,   // backward only: P_ii
-  kSG = 6,   // backward only: G log2(e) as 64 doubles (two slots)
-  kSrq = 8,  // backward only: rq
-  kSrk = 9,  // backward only: rk
-  kGdnScal = 10
+  kSq = 4,   // e^G rq / sqrt(K)
+  kSp = 5,   // from here on for the backward only: P_ii
+  kSG = 6,   // G log2(e) as 64 doubles (two slots)
+  kSe = 8,   // e^{G_last - G} rk
+  kSrq = 9,  // rq
+  kSrk = 10,  // rk
+  kGdnScal = 12  // (whole KB)
 };
 
 template <typename T>

@@ -110,10 +110,12 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
       const bool ok = lane < L;
       sc[kSk * kC + lane] = ok ? eg * rk : 0.f;
       sc[kSq * kC + lane] = ok ? eg * rq * scale : 0.f;
-      sc[kSe * kC + lane] = ok ? ex2((float)(Gl - G)) * rk : 0.f;
+      const float ee = ok ? ex2((float)(Gl - G)) * rk : 0.f;
+      sc[kSeb * kC + lane] = ee * b;
       sc[kSb * kC + lane] = b;
       if constexpr (BWD) {
         if (!ok) sc[kSp * kC + lane] = 0.f;
+        sc[kSe * kC + lane] = ee;
         reinterpret_cast<double*>(sc + kSG * kC)[lane] = G;
         sc[kSrq * kC + lane] = rq;
         sc[kSrk * kC + lane] = rk;
@@ -311,7 +313,7 @@ template <int K, int NP, bool BWD>
 struct GdnScanLds {
   static constexpr int NK = K / 32, PT = BWD ? 2 : 1;
   static constexpr uint32_t tok = TokTile<bf16, K>::bytes, tri = kTriElems * sizeof(bf16);
-  static constexpr int scal = (BWD ? 8 : 4) * kC * (int)sizeof(float);
+  static constexpr int scal = 4 * kC * (int)sizeof(float);  // state: slots 0..3, output: 3..6
   // state wave's buffer: k, M (hi, lo), row factors; output wave's: q, P, row factors
   static constexpr uint32_t sM = tok, sF = sM + 2 * tri, sbuf = sF + scal;
   static constexpr uint32_t oP = tok, oF = oP + PT * tri, obuf = oF + scal;
@@ -322,7 +324,7 @@ struct GdnScanLds {
 };
 
 template <int K, int V, int NP, bool BWD>
-__global__ void __launch_bounds__(NP * 128)
+__global__ void __launch_bounds__(NP * 128, BWD ? 1 : 2)  // 2: 256 registers, none of them accumulation-only
 gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
                 const float* h0, const int32_t* __restrict__ cu, const int* __restrict__ table, int N,
                 int T_, int H, int HV, const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag,
@@ -360,20 +362,15 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
       for (int e = 0; e < 4; ++e)
         S[r][e] = h0 ? h0[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] : 0.f;
     TileRaw<bf16> vr[4];
-    float gl;
     auto fetch_v = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) tile_ld(vr[t], v + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
-      gl = ws_scal[chunk(c) * (kGdnScal * kC) + kSl * kC];
     };
     fetch_v(0);
     __syncthreads();  // the first chunk's operands
-    for (int it = 0; it <= nc; ++it) {
+    __builtin_amdgcn_s_setprio(2);  // ahead of an output wave on the same SIMD
+    for (int it = 0; it < nc; ++it) {
       __syncthreads();
-      if (it == nc) {
-        __syncthreads();
-        break;
-      }
       const char* b = smem + (it & 1) * L_::sbuf;
       const bf16* sM = reinterpret_cast<const bf16*>(b + L_::sM);
       const float* sf = reinterpret_cast<const float*>(b + L_::sF);
@@ -389,12 +386,17 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
       f32x4 x[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) x[t] = tile_get(vr[t]);
-      const float el = gl;
+      // (from LDS: a scalar load in flight would turn every wait on LDS into a full one)
+      const float el = sf[kSl * kC + lane];
       if (it + 1 < nc) fetch_v(it + 1);
       // k S0, both parts of S0: it feeds the state
       Op8s<bf16> sb[NK];
 #pragma unroll
-      for (int s = 0; s < NK; ++s) make_op(sb[s], S[2 * s], S[2 * s + 1]);
+      for (int s = 0; s < NK; ++s) {
+        make_op(sb[s], S[2 * s], S[2 * s + 1]);
+        S[2 * s] *= el;  // S0 is not needed again
+        S[2 * s + 1] *= el;
+      }
       f32x4 ks[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) ks[t] = zero4();
@@ -488,9 +490,9 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * s + i;
           float f[4];
-          lds4(sf + kSe * kC + perm_row4(t, g), f);
+          lds4(sf + kSeb * kC + perm_row4(t, g), f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) ed[i][e] = f[e] * (bb[t][e] * x[t][e]);
+          for (int e = 0; e < 4; ++e) ed[i][e] = f[e] * x[t][e];
         }
         make_op(eb[s], ed[0], ed[1]);
       }
@@ -503,11 +505,6 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
         }
         stage();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          S[r][e] *= el;
-          S[r + 1][e] *= el;
-        }
-#pragma unroll
         for (int s = 0; s < 2; ++s) {
           S[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r][s].v, eb[s].lo, S[r], 0, 0, 0);
           S[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r + 1][s].v, eb[s].lo, S[r + 1], 0, 0, 0);
@@ -516,6 +513,9 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
         }
       }
     }
+    __builtin_amdgcn_s_setprio(0);
+    __syncthreads();  // the output wave's last chunk
+    __syncthreads();
     if constexpr (BWD) {
       if (dht) {
         float y = 0.f;
@@ -552,7 +552,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
     const uint32_t b = lds + L_::at_o + (c & 1) * L_::obuf;
     tok.go(b, q + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
     dma_flat<L_::PT * L_::tri, NP>(b + L_::oP, ws_frag + chunk(c) * kFrag + 2 * kTriElems, pair);
-    dma_flat<L_::scal, NP>(b + L_::oF, ws_scal + chunk(c) * (kGdnScal * kC), pair);
+    dma_flat<L_::scal, NP>(b + L_::oF, ws_scal + chunk(c) * (kGdnScal * kC) + kSb * kC, pair);
   };
   TileRaw<bf16> dr[4];
   fetch_s(0);
@@ -588,7 +588,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
     }
     const char* b = smem + L_::at_o + (c & 1) * L_::obuf;
     const bf16* sP = reinterpret_cast<const bf16*>(b + L_::oP);
-    const float* sf = reinterpret_cast<const float*>(b + L_::oF);
+    const float* sf = reinterpret_cast<const float*>(b + L_::oF);  // from slot kSb on
     if constexpr (BWD) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) dot[t] = tile_get(dr[t]);
@@ -619,7 +619,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
     read_q(0);
     float bb[4][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) lds4(sf + kSb * kC + perm_row4(t, g), bb[t]);
+    for (int t = 0; t < 4; ++t) lds4(sf +  perm_row4(t, g), bb[t]);
     Op8s<bf16> db[2];  // split: with S0 and P rounded as well, hi alone left o at 1.65x its rounding error
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -652,7 +652,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       float f[4];
-      lds4(sf + kSq * kC + perm_row4(t, g), f);
+      lds4(sf + (kSq - kSb) * kC + perm_row4(t, g), f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) qs[t][e] *= f[e];
     }
@@ -662,7 +662,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         float f[4], y[4];
-        lds4(sf + kSp * kC + perm_row4(t, g), f);
+        lds4(sf + (kSp - kSb) * kC + perm_row4(t, g), f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = row16_sum(dot[t][e] * (qs[t][e] - f[e] * bb[t][e] * pred[t][e]));
         if (l16 == 0) *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = make_float4(y[0], y[1], y[2], y[3]);
@@ -680,7 +680,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
 template <int K, bool BWD>
 struct GdnScan32Lds {
   static constexpr uint32_t tok = TokTile<float, K>::bytes, tri = kTriElems * sizeof(float);
-  static constexpr uint32_t oQ = tok, oM = 2 * tok, oS = oM + 2 * tri, total = oS + 4 * kC * sizeof(float);
+  static constexpr uint32_t oQ = tok, oM = 2 * tok, oS = oM + 2 * tri, total = oS + 8 * kC * sizeof(float);
 };
 
 template <int K, int V, int NW, bool BWD>
@@ -715,7 +715,7 @@ gdn_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, cons
     tok.go(lds, k + row, L);
     if constexpr (!BWD) tok.go(lds + L_::oQ, q + row, L);
     dma_flat<2 * L_::tri, NW>(lds + L_::oM, ws_frag + cc * kFrag, wave);
-    dma_flat<4 * kC * 4, NW>(lds + L_::oS, ws_scal + cc * (kGdnScal * kC), wave);
+    dma_flat<8 * kC * 4, NW>(lds + L_::oS, ws_scal + cc * (kGdnScal * kC), wave);
   };
   f32x4 S[RT];
 #pragma unroll
@@ -796,11 +796,11 @@ gdn_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, cons
       for (int i = 0; i < 2; ++i) {
         const int t = 2 * s + i;
         float f[4];
-        lds4(sf + kSe * kC + perm_row4(t, g), f);
+        lds4(sf + kSeb * kC + perm_row4(t, g), f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           d[i][e] = bb[t][e] * x[t][e];
-          ed[i][e] = f[e] * d[i][e];
+          ed[i][e] = f[e] * x[t][e];
         }
       }
       make_op(eb[s], ed[0], ed[1]);

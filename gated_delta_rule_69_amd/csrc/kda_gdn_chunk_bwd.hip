@@ -44,7 +44,7 @@ struct GdnRevLds {
   static constexpr size_t oQ = tok;
   static constexpr size_t oM = 2 * tok;
   static constexpr size_t oS = oM + tri;
-  static constexpr int scal = 8 * kC * (int)sizeof(float);  // row factors 0..7
+  static constexpr int scal = 12 * kC * (int)sizeof(float);  // row factors (whole KB)
   static constexpr size_t buf = oS + scal;
   static constexpr int nbuf = sizeof(T) == 2 ? 2 : 1;
   static constexpr size_t total = nbuf * buf;
