@@ -73,6 +73,7 @@ enum GdnScal : int {
   kSe = 8,   // e^{G_last - G} rk
   kSrq = 9,  // rq
   kSrk = 10,  // rk
+  kSpd = 11,  // P_ii again
   kGdnScal = 12  // (whole KB)
 };
 
@@ -394,6 +395,15 @@ __device__ __forceinline__ void lds_dma(const void* base, uint32_t off, uint32_t
                : "memory", "m0");
 }
 __device__ __forceinline__ void lds_dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// The same where the wave has issued at least N other vector memory accesses
+// (stores) behind its last transfer: they complete in order, so the last N may
+// still be under way.
+template <int N>
+__device__ __forceinline__ void lds_dma_wait_but() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// Makes the compiler wait for a loaded value here. It counts only the accesses
+// it knows of: behind a transfer its wait would include part of that.
+__device__ __forceinline__ void settle(const uint2& x) { asm volatile("" ::"v"(x.x), "v"(x.y)); }
+__device__ __forceinline__ void settle(const float& x) { asm volatile("" ::"v"(x)); }
 // byte address within LDS of a __shared__ object
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   typedef __attribute__((address_space(3))) const char lchar;
@@ -438,6 +448,38 @@ __device__ __forceinline__ void dma_flat(uint32_t dst, const void* src, int wave
     const int i = n * NW + wave;
     if (i >= BYTES / 1024) break;
     lds_dma(reinterpret_cast<const char*>(src) + 1024 * i, 16 * lane, dst + 1024 * i);
+  }
+}
+
+// ------------------------------------------------------------------ chains
+// What one workgroup of a scan works on: a chain (sequence, value head) and a
+// block of columns. 1-D grid in groups of 8 chains x NVB column blocks: the
+// blocks of a chain are 8 apart, so they run on one XCD and share its L2 for
+// k, q, M and P. Packed batches take their sequences longest first.
+struct GdnChain {
+  int ok, n, hv, h, vb, len;
+  int64_t bos, c0;  // first token; first chunk
+};
+__device__ __forceinline__ GdnChain gdn_chain(int nvb, const int32_t* cu, const int* table, int N, int T_,
+                                              int H, int HV) {
+  GdnChain r;
+  const int grp = blockIdx.x / (8 * nvb), in = blockIdx.x % (8 * nvb);
+  const int64_t chain = (int64_t)grp * 8 + in % 8;
+  r.ok = chain < (int64_t)N * HV;
+  if (!r.ok) return r;
+  r.n = cu ? table[2 + N + (int)(chain / HV)] : (int)(chain / HV);
+  r.hv = (int)(chain % HV);
+  r.h = r.hv / (HV / H);
+  r.vb = in / 8;
+  seq_range(cu, r.n, T_, &r.bos, &r.len);
+  r.c0 = cu ? table[1 + r.n] : (int64_t)r.n * ((T_ + kC - 1) / kC);
+  return r;
+}
+// empty slot: bitwise passthrough of the state (or +0.0 without one), columns col0 .. + 15
+__device__ __forceinline__ void gdn_pass(const float* h0, float* ht, size_t st, int K, int V, int col0) {
+  for (int e = threadIdx.x & 63; e < K * 16; e += 64) {
+    const size_t off = st + (size_t)(e >> 4) * V + col0 + (e & 15);
+    reinterpret_cast<uint32_t*>(ht)[off] = h0 ? reinterpret_cast<const uint32_t*>(h0)[off] : 0u;
   }
 }
 

@@ -114,7 +114,7 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
       sc[kSeb * kC + lane] = ee * b;
       sc[kSb * kC + lane] = b;
       if constexpr (BWD) {
-        if (!ok) sc[kSp * kC + lane] = 0.f;
+        if (!ok) sc[kSp * kC + lane] = sc[kSpd * kC + lane] = 0.f;
         sc[kSe * kC + lane] = ee;
         reinterpret_cast<double*>(sc + kSG * kC)[lane] = G;
         sc[kSrq * kC + lane] = rq;
@@ -139,6 +139,7 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
           p = qk[J][e] * d * sRq[i] * scale;
           if (BWD && i == jj) {
             ws_scal[ch * (kGdnScal * kC) + kSp * kC + i] = p;
+            ws_scal[ch * (kGdnScal * kC) + kSpd * kC + i] = p;
             p = 0.f;
           }
         }
@@ -263,37 +264,6 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
 }
 
 // ------------------------------------------------------------------ scan
-// What one workgroup of a scan works on: a chain (sequence, value head) and a
-// block of columns. 1-D grid in groups of 8 chains x NVB column blocks: the
-// blocks of a chain are 8 apart, so they run on one XCD and share its L2 for
-// k, q, M and P. Packed batches take their sequences longest first.
-struct GdnChain {
-  int ok, n, hv, h, vb, len;
-  int64_t bos, c0;  // first token; first chunk
-};
-__device__ __forceinline__ GdnChain gdn_chain(int nvb, const int32_t* cu, const int* table, int N, int T_,
-                                              int H, int HV) {
-  GdnChain r;
-  const int grp = blockIdx.x / (8 * nvb), in = blockIdx.x % (8 * nvb);
-  const int64_t chain = (int64_t)grp * 8 + in % 8;
-  r.ok = chain < (int64_t)N * HV;
-  if (!r.ok) return r;
-  r.n = cu ? table[2 + N + (int)(chain / HV)] : (int)(chain / HV);
-  r.hv = (int)(chain % HV);
-  r.h = r.hv / (HV / H);
-  r.vb = in / 8;
-  seq_range(cu, r.n, T_, &r.bos, &r.len);
-  r.c0 = cu ? table[1 + r.n] : (int64_t)r.n * ((T_ + kC - 1) / kC);
-  return r;
-}
-// empty slot: bitwise passthrough of the state (or +0.0 without one), columns col0 .. + 15
-__device__ __forceinline__ void gdn_pass(const float* h0, float* ht, size_t st, int K, int V, int col0) {
-  for (int e = threadIdx.x & 63; e < K * 16; e += 64) {
-    const size_t off = st + (size_t)(e >> 4) * V + col0 + (e & 15);
-    reinterpret_cast<uint32_t*>(ht)[off] = h0 ? reinterpret_cast<const uint32_t*>(h0)[off] : 0u;
-  }
-}
-
 // bf16. Two waves per 16 columns. The state wave keeps S (K / 16 accumulator
 // tiles) and walks the recurrence: every product of a chunk takes an
 // accumulator result of the wave itself as its right operand, so the
@@ -559,8 +529,16 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
   lds_dma_wait();
   __syncthreads();
   for (int it = 0; it <= nc; ++it) {
-    lds_dma_wait();
+    // behind the previous round's transfers: the stores of chunk it - 2, a full
+    // one (O: 4; BWD: S0 8 and Y 4)
+    if (it >= 2) lds_dma_wait_but<BWD ? RT + 4 : 4>();
+    else lds_dma_wait();
     __syncthreads();
+    if constexpr (BWD) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (it > 0) settle(dr[t].r);
+    }
     if (it + 1 < nc) fetch_s(it + 1);
     if (it < nc) fetch_o(it);
     const int c = it - 1;

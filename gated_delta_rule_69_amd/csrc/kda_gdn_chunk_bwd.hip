@@ -37,206 +37,530 @@
 namespace kda {
 
 // ------------------------------------------------------------------ reverse scan
-template <typename T, int K>
+// bf16. Two waves per 16 columns, as in the forward scan. The state wave keeps
+// dS and walks
+//   x = e^{G_last - G} k dS + p,  D' = x - M^T b (x + P_ii dO),  D = D' + P_ii dO,
+//   dS = e^{G_last} dS + Z - (e^G k)^T b D
+// with p = P^T dO (P strictly lower) and Z = (e^G q~)^T dO from the side wave,
+// which works a chunk ahead on these (they do not depend on dS) and a chunk
+// behind on what leaves: dS, D and dv = b D in memory, and the columns' share
+// of dg. It also issues the transfers of left operands into LDS. Two barriers
+// per chunk: at its top (operands, p and Z in LDS), and after the state wave
+// has taken p and Z and the side wave the previous chunk's dS and D'; the side
+// wave does its own products behind that one, where the state wave does not
+// wait for them.
+template <int K, int NP>
 struct GdnRevLds {
-  static constexpr size_t tok = TokTile<T, K>::bytes;
-  static constexpr size_t tri = GdnWs<T>::bwd * sizeof(T);  // M^T, P^T (all parts)
-  static constexpr size_t oQ = tok;
-  static constexpr size_t oM = 2 * tok;
-  static constexpr size_t oS = oM + tri;
-  static constexpr int scal = 12 * kC * (int)sizeof(float);  // row factors (whole KB)
-  static constexpr size_t buf = oS + scal;
-  static constexpr int nbuf = sizeof(T) == 2 ? 2 : 1;
-  static constexpr size_t total = nbuf * buf;
+  static constexpr int NK = K / 32, RT = K / 16;
+  static constexpr uint32_t tok = TokTile<bf16, K>::bytes, tri = kTriElems * sizeof(bf16), scal = 1024;
+  // state wave: k, M^T (hi, lo), row factors 0..3 and 8..11, twice
+  static constexpr uint32_t sM = tok, sF = sM + 2 * tri, sE = sF + scal, sbuf = sE + scal;
+  // side wave: q, P^T (hi, lo), row factors 3..6, twice
+  static constexpr uint32_t oP = tok, oF = oP + 2 * tri, obuf = oF + scal;
+  static constexpr uint32_t at_o = 2 * sbuf, at_x = at_o + 2 * obuf;
+  // exchange of a pair: dS (high part), D'; p, Z
+  static constexpr uint32_t xS = NK * 1024, xD = 4 * 1024, xp = 4 * 1024, xZ = RT * 1024;
+  static constexpr uint32_t xbuf = xS + xD + xp + xZ;
+  static constexpr uint32_t total = at_x + NP * xbuf;
 };
 
-template <typename T, int K, int V, int NW>
-__global__ void __launch_bounds__(NW * 64)
-gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                    const T* __restrict__ dO, const float* __restrict__ dht, const int32_t* __restrict__ cu,
+// c += X^T b with the six fragments of a transposed triangle (frag_up order)
+__device__ __forceinline__ void mma_up(const Op8<bf16> (&a)[6], const bf16x8 (&b)[2], f32x4 (&c)[4]) {
+#pragma unroll
+  for (int s = 1; s >= 0; --s)
+#pragma unroll
+    for (int t = 0; t < 2 * s + 2; ++t)
+      c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[frag_up(t, s)].v, b[s], c[t], 0, 0, 0);
+}
+
+template <int K, int V, int NP>
+__global__ void __launch_bounds__(NP * 128)
+gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
+                    const bf16* __restrict__ dO, const float* __restrict__ dht, const int32_t* __restrict__ cu,
                     const int* __restrict__ table, int N, int T_, int H, int HV,
-                    const float* __restrict__ ws_scal, const T* __restrict__ ws_bwd,
-                    T* __restrict__ dv, float* __restrict__ dh0, T* __restrict__ ws_dS,
-                    T* __restrict__ ws_D, float* __restrict__ ws_tok, const float* __restrict__ ws_end) {
+                    const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag, bf16* __restrict__ dv,
+                    float* __restrict__ dh0, bf16* __restrict__ ws_dS, bf16* __restrict__ ws_D,
+                    float* __restrict__ ws_tok, const float* __restrict__ ws_end) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  __shared__ __attribute__((aligned(16))) float s_tok[NW][kC];
-  using Lds = GdnRevLds<T, K>;
-  using TT = TokTile<T, K>;
-  constexpr int NK = K / 32, RT = K / 16, BV = 16 * NW, NVB = V / BV, PT = GdnWs<T>::kParts;
-  constexpr bool kGate = GdnWs<T>::kScanGate;
-  const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int grp = blockIdx.x / (8 * NVB), in = blockIdx.x % (8 * NVB);
-  const int64_t chain = (int64_t)grp * 8 + in % 8;
-  if (chain >= (int64_t)N * HV) return;
-  const int n = cu ? table[2 + N + (int)(chain / HV)] : (int)(chain / HV);
-  const int hv = (int)(chain % HV), h = hv / (HV / H);
-  const int col0 = (in / 8) * BV + 16 * wave;
-  int64_t bos;
-  int len;
-  seq_range(cu, n, T_, &bos, &len);
-  const size_t st = ((size_t)n * HV + hv) * (size_t)K * V;
+  __shared__ __attribute__((aligned(16))) float s_tok[NP][kC];
+  using L_ = GdnRevLds<K, NP>;
+  using TT = TokTile<bf16, K>;
+  constexpr int NK = K / 32, RT = K / 16, BV = 16 * NP, NVB = V / BV;
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int pair = wave % NP;
+  const GdnChain ch = gdn_chain(NVB, cu, table, N, T_, H, HV);
+  if (!ch.ok) return;
+  const int col0 = ch.vb * BV + 16 * pair, hv = ch.hv, len = ch.len;
+  const size_t st = ((size_t)ch.n * HV + hv) * (size_t)K * V;
   if (len <= 0) {
-    if (!dh0) return;
-    for (int e = lane; e < K * 16; e += 64) {
-      const size_t off = st + (size_t)(e >> 4) * V + col0 + (e & 15);
-      dh0[off] = dht ? dht[off] : 0.f;
-    }
+    if (dh0 && wave < NP) gdn_pass(dht, dh0, st, K, V, col0);
     return;
   }
   const int nc = (len + kC - 1) / kC;
-  const int64_t c0 = cu ? table[1 + n] : (int64_t)n * ((T_ + kC - 1) / kC);
+  auto chunk = [&](int c) { return (size_t)(ch.c0 + c) * HV + hv; };
+  auto tokens = [&](int c) { return min(kC, len - c * kC); };
+  auto vrow = [&](int c) { return ((ch.bos + (int64_t)c * kC) * HV + hv) * V; };
+  char* xch = smem + L_::at_x + pair * L_::xbuf;
+  char* xp = xch + L_::xS + L_::xD;
+  char* xZ = xp + L_::xp;
 
-  const uint32_t lds = lds_addr(smem);
-  const TokDma<T, K, NW> tok((uint32_t)(H * K * sizeof(T)), wave);
-  auto fetch = [&](int c, uint32_t b) {
-    const size_t ch = (size_t)(c0 + c) * HV + hv;
-    const int64_t row = ((bos + (int64_t)c * kC) * H + h) * K;
-    const int L = min(kC, len - c * kC);
-    tok.go(b, k + row, L);
-    tok.go(b + Lds::oQ, q + row, L);
-    dma_flat<(int)Lds::tri, NW>(b + Lds::oM, ws_bwd + ch * GdnWs<T>::bwd, wave);
-    dma_flat<Lds::scal, NW>(b + Lds::oS, ws_scal + ch * (kGdnScal * kC), wave);
-  };
-  TileRaw<T> dr[4], vr[4];
-  float gl, od;
-  auto fetch_do = [&](int c) {
-    const int L = min(kC, len - c * kC);
-    const int64_t at = ((bos + (int64_t)c * kC) * HV + hv) * V;
+  if (wave < NP) {
+    f32x4 S[RT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      tile_ld(dr[t], dO + at, HV * V, perm_row4(t, g), col0, L);
-      if constexpr (kGate) tile_ld(vr[t], v + at, HV * V, perm_row4(t, g), col0, L);
-    }
-    if constexpr (kGate) od = ws_tok[(((size_t)(c0 + c) * HV + hv) * (V / 16) + (col0 >> 4)) * kC + lane];
-    gl = ws_scal[((size_t)(c0 + c) * HV + hv) * (kGdnScal * kC) + kSl * kC];
-  };
-
-  f32x4 S[RT];  // dS
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+      for (int e = 0; e < 4; ++e)
+        S[r][e] = dht ? dht[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] : 0.f;
+    TileRaw<bf16> dr[4];
+    auto fetch_do = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      S[r][e] = dht ? dht[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] : 0.f;
-
-  // sum over the tokens behind this chunk of <o, dO> - <v, dv>, these columns
-  double behind = kGate && dht ? (double)ws_end[((size_t)n * HV + hv) * (V / 16) + (col0 >> 4)] : 0.;
-  int buf = 0;
-  fetch(nc - 1, lds);
-  fetch_do(nc - 1);
-  for (int c = nc - 1; c >= 0; --c) {
-    const char* b = smem + buf * Lds::buf;
-    lds_dma_wait();
-    __syncthreads();
-    if (Lds::nbuf == 2) {
-      buf ^= 1;
-      if (c > 0) fetch(c - 1, lds + buf * (uint32_t)Lds::buf);
-    }
-    const float* sf = reinterpret_cast<const float*>(b + Lds::oS);
-    const T* sM = reinterpret_cast<const T*>(b + Lds::oM);
-    const T* sP = sM + PT * kTriElems;
-    const size_t ch = (size_t)(c0 + c) * HV + hv;
-    const int L = min(kC, len - c * kC);
-    f32x4 dot[4];
-    Op8<T> dop[2];
+      for (int t = 0; t < 4; ++t) tile_ld(dr[t], dO + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
+    };
+    fetch_do(nc - 1);
+    __syncthreads();  // the last chunk's operands
+    __builtin_amdgcn_s_setprio(2);
+    for (int c = nc - 1, buf = 0; c >= 0; --c, buf ^= 1) {
+      __syncthreads();
+      const char* b = smem + buf * L_::sbuf;
+      const bf16* sM = reinterpret_cast<const bf16*>(b + L_::sM);
+      const float* sf = reinterpret_cast<const float*>(b + L_::sF);
+      const float* se = reinterpret_cast<const float*>(b + L_::sE);  // from slot kSe on
+      Op8<bf16> ka[NK][4], ml[2][6];
+      auto read_k = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) dot[t] = tile_get(dr[t]);
+        for (int t = 0; t < 4; ++t) TT::rows(ka[s][t], b, t, s);
+      };
+      auto read_m = [&](int f) __attribute__((always_inline)) {
+        ld_op(ml[0][f], sM + f * kFragElems + lane * 8);
+        ld_op(ml[1][f], sM + kTriElems + f * kFragElems + lane * 8);
+      };
+      read_k(0);
+      read_k(1);
+      f32x4 pd[4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) tile_op(dop[s], dr[2 * s], dr[2 * s + 1]);
-    f32x4 vt[4];
-    if constexpr (kGate) {
+      for (int t = 0; t < 4; ++t) pd[t] = tile_get(dr[t]);
+      const float el = sf[kSl * kC + lane];
+      if (c > 0) fetch_do(c - 1);
+      Op8s<bf16> sb[NK];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) vt[t] = tile_get(vr[t]);
-    }
-    const float el = gl, od_c = kGate ? od : 0.f;
-    if (c > 0) fetch_do(c - 1);
-
+      for (int s = 0; s < NK; ++s) make_op(sb[s], S[2 * s], S[2 * s + 1]);
 #pragma unroll
-    for (int r = 0; r < RT; ++r) tile_st(ws_dS + ch * K * V, V, perm_row4(r, g), col0, K, S[r]);
-    // dDelta = P^T dO + e^{G_last - G} (k dS), P's diagonal apart
-    f32x4 x[4], p[4];
+      for (int r = 0; r < RT; ++r) {
+        const f32x4 z = *reinterpret_cast<const f32x4*>(xZ + (r * 64 + lane) * 16);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) x[t] = p[t] = zero4();
-#pragma unroll
-    for (int s = 0; s < NK; ++s) {
-      Op8s<T> sb;
-      make_op(sb, S[2 * s], S[2 * s + 1]);
+        for (int e = 0; e < 4; ++e) S[r][e] = fmaf(S[r][e], el, z[e]);
+      }
+      f32x4 ks[4], x[4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        Op8<T> a;
-        TT::rows(a, b, t, s);
-        x[t] = mma8s(a, sb, x[t]);
+        ks[t] = zero4();
+        x[t] = *reinterpret_cast<const f32x4*>(xp + (t * 64 + lane) * 16);
       }
-    }
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+      for (int s = 0; s < NK; ++s) {
+        stage();
+        if (s + 2 < NK) {
+          read_k(s + 2);
+        } else {
+          read_m(2 * (s + 2 - NK));
+          read_m(2 * (s + 2 - NK) + 1);
+        }
+        stage();
+        mma_rows(ka[s], sb[s], ks);
+      }
+      stage();
+      read_m(4);
+      read_m(5);
+      __syncthreads();  // p, Z and the previous chunk's dS, D' are taken
 #pragma unroll
-      for (int s = (t >> 1); s < 2; ++s) {
-        Op8<T> a;
+      for (int s = 0; s < NK; ++s) *reinterpret_cast<bf16x8*>(xch + (s * 64 + lane) * 16) = sb[s].hi;
+      f32x4 bb[4];
 #pragma unroll
-        for (int pt = PT - 1; pt >= 0; --pt) {
-          ld_op(a, sP + pt * kTriElems + frag_up(t, s) * kFragElems + lane * 8);
-          p[t] = mma8(a, dop[s], p[t]);
+      for (int t = 0; t < 4; ++t) {
+        float f[4], w[4], y[4];
+        lds4(se + perm_row4(t, g), f);
+        lds4(sf + kSb * kC + perm_row4(t, g), w);
+        lds4(se + (kSpd - kSe) * kC + perm_row4(t, g), y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[t][e] = fmaf(f[e], ks[t][e], x[t][e]);
+          pd[t][e] *= y[e];
+          bb[t][e] = w[e];
         }
       }
-    f32x4 bb[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      float f[4], w[4], pd[4];
-      lds4(sf + kSe * kC + perm_row4(t, g), f);
-      lds4(sf + kSb * kC + perm_row4(t, g), w);
-      lds4(sf + kSp * kC + perm_row4(t, g), pd);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[t][e] = fmaf(f[e], x[t][e], p[t][e]);
-        p[t][e] = pd[e] * dot[t][e];
-        bb[t][e] = w[e];
-      }
-    }
-    // D' = dDelta' - M^T (b dDelta), D = D' + P_ii dO
-    {
-      Op8s<T> rb[2];
+      Op8s<bf16> rb[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         f32x4 a0, a1;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          a0[e] = -bb[2 * s][e] * (x[2 * s][e] + p[2 * s][e]);
-          a1[e] = -bb[2 * s + 1][e] * (x[2 * s + 1][e] + p[2 * s + 1][e]);
+          a0[e] = -bb[2 * s][e] * (x[2 * s][e] + pd[2 * s][e]);
+          a1[e] = -bb[2 * s + 1][e] * (x[2 * s + 1][e] + pd[2 * s + 1][e]);
         }
         make_op(rb[s], a0, a1);
       }
+      {
+        const bf16x8 hi[2] = {rb[0].hi, rb[1].hi}, lo[2] = {rb[0].lo, rb[1].lo};
+        mma_up(ml[0], lo, x);
+        mma_up(ml[1], hi, x);
+        mma_up(ml[0], hi, x);
+      }
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(xch + L_::xS + (t * 64 + lane) * 16) = x[t];
+      Op8<bf16> kc[RT][2];
+      auto read_kc = [&](int r) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = (t >> 1); s < 2; ++s) {
-          Op8<T> a;
-          if constexpr (sizeof(T) == 2) {
-            ld_op(a, sM + kTriElems + frag_up(t, s) * kFragElems + lane * 8);
-            x[t] = mma8h(a, rb[s], x[t]);
-          }
-          ld_op(a, sM + frag_up(t, s) * kFragElems + lane * 8);
-          x[t] = mma8s(a, rb[s], x[t]);
+        for (int s = 0; s < 2; ++s) TT::cols(kc[r][s], b, r, s);
+      };
+      read_kc(0);
+      read_kc(1);
+      Op8s<bf16> eb[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        f32x4 ed[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = 2 * s + i;
+          float f[4];
+          lds4(sf + kSk * kC + perm_row4(t, g), f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ed[i][e] = -(f[e] * bb[t][e]) * (x[t][e] + pd[t][e]);
         }
+        make_op(eb[s], ed[0], ed[1]);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; r += 2) {
+        stage();
+        if (r + 2 < RT) {
+          read_kc(r + 2);
+          read_kc(r + 3);
+        }
+        stage();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          S[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r][s].v, eb[s].lo, S[r], 0, 0, 0);
+          S[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r + 1][s].v, eb[s].lo, S[r + 1], 0, 0, 0);
+          S[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r][s].v, eb[s].hi, S[r], 0, 0, 0);
+          S[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kc[r + 1][s].v, eb[s].hi, S[r + 1], 0, 0, 0);
+        }
+      }
     }
-    if constexpr (kGate) {
+    __builtin_amdgcn_s_setprio(0);
+    __syncthreads();  // the side wave's last chunk
+    __syncthreads();
+    if (dh0) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dh0[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] = S[r][e];
+    }
+    return;
+  }
+
+  // ---- side wave
+  const uint32_t lds = lds_addr(smem);
+  const TokDma<bf16, K, NP> tok((uint32_t)(H * K * sizeof(bf16)), pair);
+  auto fetch_s = [&](int c, int buf) __attribute__((always_inline)) {
+    const uint32_t b = lds + buf * L_::sbuf;
+    tok.go(b, k + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
+    dma_flat<2 * L_::tri, NP>(b + L_::sM, ws_frag + chunk(c) * GdnWs<bf16>::bwd, pair);
+    dma_flat<L_::scal, NP>(b + L_::sF, ws_scal + chunk(c) * (kGdnScal * kC), pair);
+    dma_flat<L_::scal, NP>(b + L_::sE, ws_scal + chunk(c) * (kGdnScal * kC) + kSe * kC, pair);
+  };
+  auto fetch_o = [&](int c) __attribute__((always_inline)) {
+    const uint32_t b = lds + L_::at_o + (c & 1) * L_::obuf;
+    tok.go(b, q + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
+    dma_flat<2 * L_::tri, NP>(b + L_::oP, ws_frag + chunk(c) * GdnWs<bf16>::bwd + 2 * kTriElems, pair);
+    dma_flat<L_::scal, NP>(b + L_::oF, ws_scal + chunk(c) * (kGdnScal * kC) + kSb * kC, pair);
+  };
+  TileRaw<bf16> dn[4];  // dO of the chunk ahead
+  auto fetch_dn = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) tile_ld(dn[t], dO + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
+  };
+  f32x4 p[4], Z[RT];
+  auto ahead = [&](int c) __attribute__((always_inline)) {  // p and Z of chunk c
+    const char* ob = smem + L_::at_o + (c & 1) * L_::obuf;
+    const bf16* sP = reinterpret_cast<const bf16*>(ob + L_::oP);
+    const float* of = reinterpret_cast<const float*>(ob + L_::oF);  // from slot kSb on
+    Op8<bf16> pf[2][6];
+#pragma unroll
+    for (int f = 0; f < 6; ++f)
+#pragma unroll
+      for (int pt = 0; pt < 2; ++pt) ld_op(pf[pt][f], sP + pt * kTriElems + f * kFragElems + lane * 8);
+    Op8<bf16> dop[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) tile_op(dop[s], dn[2 * s], dn[2 * s + 1]);
+    Op8s<bf16> qb[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      f32x4 d[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 w = __builtin_bit_cast(uint4, dop[s].v);
+        d[i] = unpack4(i ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y));
+        float f[4];
+        lds4(of + (kSq - kSb) * kC + perm_row4(2 * s + i, g), f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[i][e] *= f[e];
+      }
+      make_op(qb[s], d[0], d[1]);
+    }
+    if (c > 0) fetch_dn(c - 1);
+    stage();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) p[t] = zero4();
+    const bf16x8 dd[2] = {dop[0].v, dop[1].v};
+    mma_up(pf[1], dd, p);
+    mma_up(pf[0], dd, p);
+    Op8<bf16> qc[RT][2];
+    auto read_qc = [&](int r) __attribute__((always_inline)) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) TT::cols(qc[r][s], ob, r, s);
+    };
+    read_qc(0);
+    read_qc(1);
+#pragma unroll
+    for (int r = 0; r < RT; r += 2) {
+      stage();
+      if (r + 2 < RT) {
+        read_qc(r + 2);
+        read_qc(r + 3);
+      }
+      stage();
+      Z[r] = Z[r + 1] = zero4();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        Z[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r][s].v, qb[s].lo, Z[r], 0, 0, 0);
+        Z[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r + 1][s].v, qb[s].lo, Z[r + 1], 0, 0, 0);
+        Z[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r][s].v, qb[s].hi, Z[r], 0, 0, 0);
+        Z[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r + 1][s].v, qb[s].hi, Z[r + 1], 0, 0, 0);
+      }
+    }
+  };
+  auto put = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(xp + (t * 64 + lane) * 16) = p[t];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(xZ + (r * 64 + lane) * 16) = Z[r];
+  };
+  // sum over the tokens behind a chunk of the tokens' scalars, these columns
+  double behind = dht ? (double)ws_end[((size_t)ch.n * HV + hv) * (V / 16) + (col0 >> 4)] : 0.;
+  // prologue: operands, p and Z of the last chunk
+  fetch_s(nc - 1, 0);
+  fetch_o(nc - 1);
+  if (nc > 1) fetch_o(nc - 2);
+  fetch_dn(nc - 1);
+  lds_dma_wait();
+  __syncthreads();
+  ahead(nc - 1);
+  put();
+  TileRaw<bf16> vb[4], db[4];  // v and dO of the chunk behind, fetched a round early
+  float bw[4][4], pw[4][4], od = 0.f;
+  auto fetch_b = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      tile_ld(vb[t], v + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
+      tile_ld(db[t], dO + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
+      const float* f = ws_scal + chunk(c) * (kGdnScal * kC);
+      lds4(f + kSb * kC + perm_row4(t, g), bw[t]);
+      lds4(f + kSp * kC + perm_row4(t, g), pw[t]);
+    }
+    od = ws_tok[(chunk(c) * (V / 16) + (col0 >> 4)) * kC + lane];
+  };
+  for (int c = nc - 1, buf = 0; c >= -1; --c, buf ^= 1) {
+    const int cb = c + 1;  // the chunk behind
+    // behind the previous round's transfers, if that round had a chunk behind:
+    // its stores (dS RT, D 4, share of dg 1)
+    if (cb + 1 < nc) lds_dma_wait_but<RT + 5>();
+    else lds_dma_wait();
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (c > 0) settle(dn[t].r);
+      if (cb < nc) {
+        settle(vb[t].r);
+        settle(db[t].r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          settle(bw[t][e]);
+          settle(pw[t][e]);
+        }
+      }
+    }
+    if (cb < nc) settle(od);
+    if (c > 0) fetch_s(c - 1, buf ^ 1);
+    if (c > 1) fetch_o(c - 2);
+    uint4 sh[NK];
+    f32x4 x[4];
+    if (cb < nc) {
+#pragma unroll
+      for (int s = 0; s < NK; ++s) sh[s] = *reinterpret_cast<const uint4*>(xch + (s * 64 + lane) * 16);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) x[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + (t * 64 + lane) * 16);
+    }
+    __syncthreads();
+    f32x4 dd[4];
+    double y = 0.;
+    if (cb < nc) {  // the values of the chunk behind; their stores come last
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        float y[4];
+        const f32x4 vt = tile_get(vb[t]), dt = tile_get(db[t]);
+        float z[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = row16_sum(bb[t][e] * x[t][e] * vt[t][e]);
+        for (int e = 0; e < 4; ++e) {
+          z[e] = row16_sum(bw[t][e] * x[t][e] * vt[e]);
+          x[t][e] = fmaf(pw[t][e], dt[e], x[t][e]);
+          dd[t][e] = x[t][e] * bw[t][e];
+        }
         if (l16 == 0)
-          *reinterpret_cast<float4*>(&s_tok[wave][perm_row4(t, g)]) = make_float4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<float4*>(&s_tok[pair][perm_row4(t, g)]) = make_float4(z[0], z[1], z[2], z[3]);
+      }
+      // the columns' share of dg: lane = token, sums from the sequence's end
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      y = lane < tokens(cb) ? (double)od - (double)s_tok[pair][lane] : 0.;
+#pragma unroll
+      for (int i = 1; i < 64; i <<= 1) {
+        const double z = __shfl_down(y, i);
+        if (lane + i < 64) y += z;
+      }
+      y += behind;
+      behind = __shfl(y, 0);
+    }
+    stage();
+    if (c >= 0) fetch_b(c);
+    if (c > 0) {
+      ahead(c - 1);
+      put();
+    }
+    asm volatile("" ::: "memory");  // every load above, the stores below
+    if (cb < nc) {
+      bf16* ds = ws_dS + chunk(cb) * K * V;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const uint2 w = quad_transpose((r & 1) ? make_uint2(sh[r >> 1].z, sh[r >> 1].w)
+                                               : make_uint2(sh[r >> 1].x, sh[r >> 1].y));
+        *reinterpret_cast<uint2*>(ds + (uint32_t)((perm_row4(r, g) + (l16 & 3)) * V + col0 + 4 * (l16 >> 2))) = w;
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        tile_st(ws_D + chunk(cb) * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+        tile_st(dv + vrow(cb), HV * V, perm_row4(t, g), col0, tokens(cb), dd[t]);
+      }
+      ws_tok[(chunk(cb) * (V / 16) + (col0 >> 4)) * kC + lane] = (float)y;
+    }
+  }
+}
+
+// FP32: one wave per 16 columns, FP32 matrix cores, one operand buffer.
+template <int K>
+struct GdnRev32Lds {
+  static constexpr uint32_t tok = TokTile<float, K>::bytes, tri = 2 * kTriElems * sizeof(float);
+  static constexpr uint32_t oQ = tok, oM = 2 * tok, oS = oM + tri, total = oS + kGdnScal * kC * sizeof(float);
+};
+
+template <int K, int V, int NW>
+__global__ void __launch_bounds__(NW * 64)
+gdn_rev_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dO,
+                      const float* __restrict__ dht, const int32_t* __restrict__ cu,
+                      const int* __restrict__ table, int N, int T_, int H, int HV,
+                      const float* __restrict__ ws_scal, const float* __restrict__ ws_frag,
+                      float* __restrict__ dv, float* __restrict__ dh0, float* __restrict__ ws_dS,
+                      float* __restrict__ ws_D) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  using L_ = GdnRev32Lds<K>;
+  using TT = TokTile<float, K>;
+  constexpr int NK = K / 32, RT = K / 16, BV = 16 * NW, NVB = V / BV;
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const GdnChain ch = gdn_chain(NVB, cu, table, N, T_, H, HV);
+  if (!ch.ok) return;
+  const int col0 = ch.vb * BV + 16 * wave, hv = ch.hv, len = ch.len;
+  const size_t st = ((size_t)ch.n * HV + hv) * (size_t)K * V;
+  if (len <= 0) {
+    if (dh0) gdn_pass(dht, dh0, st, K, V, col0);
+    return;
+  }
+  const int nc = (len + kC - 1) / kC;
+  const uint32_t lds = lds_addr(smem);
+  const TokDma<float, K, NW> tok((uint32_t)(H * K * sizeof(float)), wave);
+  const float* sf = reinterpret_cast<const float*>(smem + L_::oS);
+  const float* sM = reinterpret_cast<const float*>(smem + L_::oM);
+  const float* sP = sM + kTriElems;
+  f32x4 S[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      S[r][e] = dht ? dht[st + (size_t)(perm_row4(r, g) + e) * V + col0 + l16] : 0.f;
+  for (int c = nc - 1; c >= 0; --c) {
+    if (c < nc - 1) __syncthreads();  // every wave is done with the buffer
+    const size_t cc = (size_t)(ch.c0 + c) * HV + hv;
+    const int64_t row = ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, at = ((ch.bos + (int64_t)c * kC) * HV + hv) * V;
+    const int L = min(kC, len - c * kC);
+    tok.go(lds, k + row, L);
+    tok.go(lds + L_::oQ, q + row, L);
+    dma_flat<(int)L_::tri, NW>(lds + L_::oM, ws_frag + cc * GdnWs<float>::bwd, wave);
+    dma_flat<kGdnScal * kC * 4, NW>(lds + L_::oS, ws_scal + cc * (kGdnScal * kC), wave);
+    f32x4 dot[4], x[4], p[4], bb[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      TileRaw<float> r;
+      tile_ld(r, dO + at, HV * V, perm_row4(t, g), col0, L);
+      dot[t] = r.r;
+      x[t] = p[t] = zero4();
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) tile_st(ws_dS + cc * K * V, V, perm_row4(r, g), col0, K, S[r]);
+    lds_dma_wait();
+    __syncthreads();
+    const float el = sf[kSl * kC];
+#pragma unroll
+    for (int s = 0; s < NK; ++s) {
+      Op8s<float> sb;
+      make_op(sb, S[2 * s], S[2 * s + 1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        Op8<float> a;
+        TT::rows(a, smem, t, s);
+        x[t] = mma8s(a, sb, x[t]);
+      }
+    }
+    Op8s<float> dop[2], rb[2], qb[2], kb[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) make_op(dop[s], dot[2 * s], dot[2 * s + 1]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int s = (t >> 1); s < 2; ++s) {
+        Op8<float> a;
+        ld_op(a, sP + frag_up(t, s) * kFragElems + lane * 8);
+        p[t] = mma8s(a, dop[s], p[t]);
+      }
+      float f[4], w[4], y[4];
+      lds4(sf + kSe * kC + perm_row4(t, g), f);
+      lds4(sf + kSb * kC + perm_row4(t, g), w);
+      lds4(sf + kSp * kC + perm_row4(t, g), y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[t][e] = fmaf(y[e], dot[t][e], fmaf(f[e], x[t][e], p[t][e]));  // dDelta
+        bb[t][e] = w[e];
       }
     }
 #pragma unroll
+    for (int s = 0; s < 2; ++s) make_op(rb[s], -bb[2 * s] * x[2 * s], -bb[2 * s + 1] * x[2 * s + 1]);
+#pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[t][e] += p[t][e];
+      for (int s = (t >> 1); s < 2; ++s) {
+        Op8<float> a;
+        ld_op(a, sM + frag_up(t, s) * kFragElems + lane * 8);
+        x[t] = mma8s(a, rb[s], x[t]);
+      }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) tile_st(ws_D + ch * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
-    // dv = E = b D; dS0 = e^{G_last} dS + q^T (e^G rq/sqrt(K) dO) - k^T (e^G rk E)
-    Op8s<T> qb[2], kb[2];
+    for (int t = 0; t < 4; ++t) tile_st(ws_D + cc * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       f32x4 eq[2], ek[2];
@@ -252,14 +576,10 @@ gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
           eq[i][e] = fq[e] * dot[t][e];
           ek[i][e] = -fk[e] * x[t][e];
         }
+        tile_st(dv + at, HV * V, perm_row4(t, g), col0, L, x[t]);
       }
       make_op(qb[s], eq[0], eq[1]);
       make_op(kb[s], ek[0], ek[1]);
-    }
-    T* vb = dv + ((bos + (int64_t)c * kC) * HV + hv) * V;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      tile_st(vb, HV * V, perm_row4(t, g), col0, L, x[t]);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -267,29 +587,12 @@ gdn_rev_scan_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
       for (int e = 0; e < 4; ++e) S[r][e] *= el;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        Op8<T> a;
-        TT::cols(a, b + Lds::oQ, r, s);
+        Op8<float> a;
+        TT::cols(a, smem + L_::oQ, r, s);
         S[r] = mma8s(a, qb[s], S[r]);
-        TT::cols(a, b, r, s);
+        TT::cols(a, smem, r, s);
         S[r] = mma8s(a, kb[s], S[r]);
       }
-    }
-    // the columns' share of dg: lane = token, sums from the sequence's end
-    if constexpr (kGate) {
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      double y = lane < L ? (double)od_c - (double)s_tok[wave][lane] : 0.;
-#pragma unroll
-      for (int i = 1; i < 64; i <<= 1) {
-        const double z = __shfl_down(y, i);
-        if (lane + i < 64) y += z;
-      }
-      y += behind;
-      behind = __shfl(y, 0);
-      ws_tok[(ch * (V / 16) + (col0 >> 4)) * kC + lane] = (float)y;
-    }
-    if (Lds::nbuf == 1 && c > 0) {
-      __syncthreads();
-      fetch(c - 1, lds);
     }
   }
   if (dh0) {
@@ -666,17 +969,32 @@ gdn_par_kernel(const float* __restrict__ par, const int* __restrict__ table, int
   }
 }
 
-template <typename T, int K, int V, int NW>
+template <int K, int V, int NP>
 static hipError_t rev_t(const kda_dims& d, const void* q, const void* k, const void* v, const void* dO,
-                        const float* dht, const int32_t* cu, const GdnLayout<T>& w, void* dv, float* dh0, hipStream_t s) {
-  constexpr size_t lds = GdnRevLds<T, K>::total;
-  static_assert(lds <= 160 * 1024, "LDS");
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_rev_scan_kernel<T, K, V, NW>),
+                        const float* dht, const int32_t* cu, const GdnLayout<bf16>& w, void* dv, float* dh0,
+                        hipStream_t s) {
+  constexpr size_t lds = GdnRevLds<K, NP>::total;
+  static_assert(lds + NP * kC * sizeof(float) <= 160 * 1024, "LDS");
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_rev_scan_kernel<K, V, NP>),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((gdn_rev_scan_kernel<T, K, V, NW>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NW)),
-                     dim3(64 * NW), lds, s, (const T*)q, (const T*)k, (const T*)v, (const T*)dO, dht, cu,
-                     w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (T*)dv, dh0, w.dS, w.D, w.tok, w.end);
+  hipLaunchKernelGGL((gdn_rev_scan_kernel<K, V, NP>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
+                     dim3(128 * NP), lds, s, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)dO, dht,
+                     cu, w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (bf16*)dv, dh0, w.dS, w.D, w.tok, w.end);
+  return hipGetLastError();
+}
+template <int K, int V, int NP>
+static hipError_t rev_t(const kda_dims& d, const void* q, const void* k, const void* v, const void* dO,
+                        const float* dht, const int32_t* cu, const GdnLayout<float>& w, void* dv, float* dh0,
+                        hipStream_t s) {
+  constexpr size_t lds = GdnRev32Lds<K>::total;
+  static_assert(lds <= 160 * 1024, "LDS");
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_rev_scan32_kernel<K, V, NP>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((gdn_rev_scan32_kernel<K, V, NP>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
+                     dim3(64 * NP), lds, s, (const float*)q, (const float*)k, (const float*)dO, dht, cu, w.table,
+                     d.N, d.T, d.H, d.HV, w.scal, w.fragT, (float*)dv, dh0, w.dS, w.D);
   return hipGetLastError();
 }
 
@@ -687,11 +1005,8 @@ static hipError_t gdn_bwd_kv(const kda_dims& d, const void* q, const void* k, co
                              void* ddt, void* ws, hipStream_t s) {
   const int64_t mc = max_chunks(d, cu != nullptr);
   const GdnLayout<T> w(d, cu != nullptr, ws, true);
-  const bool wide = (int64_t)d.N * d.HV * (V / 64) >= kda_host::device_cus();
   hipError_t e = hipSuccess;
-  if (d.N > 0)
-    e = wide ? rev_t<T, K, V, 4>(d, q, k, v, dO, dht, cu, w, dv, dh0, s)
-             : rev_t<T, K, V, 2>(d, q, k, v, dO, dht, cu, w, dv, dh0, s);
+  if (d.N > 0) e = rev_t<K, V, 2>(d, q, k, v, dO, dht, cu, w, dv, dh0, s);
   if (e != hipSuccess) return e;
   if (d.N > 0 && mc > 0) {
     constexpr size_t lds = 2 * TokTile<T, K>::bytes;
