@@ -254,8 +254,10 @@ __device__ __forceinline__ f32x4 unpack4(uint2 r) {
 
 // A 16 x 16 tile between row-major memory and the accumulator layout. `row4`
 // is the lane's first row (perm_row4), rows row4 .. row4 + 3, column col0 + l16;
-// element (r, c) at p + r * stride + c, rows >= rows absent (zero / not
-// written). bf16: p 8-byte aligned, stride and col0 multiples of 4. p is uniform
+// element (r, c) at p + r * stride + c. Rows from `rows` on are not written; as
+// loads they repeat the last row (unconditional loads: under a lane-dependent
+// branch each would be waited for at the branch's join), and what they feed is
+// multiplied by row factors that are zero there. bf16: p 8-byte aligned, stride and col0 multiples of 4. p is uniform
 // in the wave and 64 rows span less than 2^31 bytes (checked by the entry
 // points), so a lane's address is a scalar base and a 32-bit offset.
 template <typename T>
@@ -270,15 +272,14 @@ struct TileRaw<float> {
 };
 __device__ __forceinline__ void tile_ld(TileRaw<bf16>& t, const bf16* p, uint32_t stride, int row4,
                                         int col0, int rows) {
-  const int l16 = threadIdx.x & 15, row = row4 + (l16 & 3);
-  t.r = make_uint2(0, 0);
-  if (row < rows) t.r = *reinterpret_cast<const uint2*>(p + (row * stride + col0 + 4 * (l16 >> 2)));
+  const int l16 = threadIdx.x & 15, row = min(row4 + (l16 & 3), rows - 1);
+  t.r = *reinterpret_cast<const uint2*>(p + (row * stride + col0 + 4 * (l16 >> 2)));
 }
 __device__ __forceinline__ void tile_ld(TileRaw<float>& t, const float* p, uint32_t stride, int row4,
                                         int col0, int rows) {
   const int l16 = threadIdx.x & 15;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) t.r[e] = row4 + e < rows ? p[(uint32_t)((row4 + e) * stride + col0 + l16)] : 0.f;
+  for (int e = 0; e < 4; ++e) t.r[e] = p[(uint32_t)(min(row4 + e, rows - 1) * stride + col0 + l16)];
 }
 __device__ __forceinline__ f32x4 tile_get(const TileRaw<bf16>& t) { return unpack4(quad_transpose(t.r)); }
 __device__ __forceinline__ f32x4 tile_get(const TileRaw<float>& t) { return t.r; }
@@ -302,12 +303,36 @@ __device__ __forceinline__ void tile_st(float* p, uint32_t stride, int row4, int
     if (row4 + e < rows) p[(uint32_t)((row4 + e) * stride + col0 + l16)] = x[e];
 }
 
+// A 16 x 16 tile (rows of tile r, columns 16 cb .. + 15 of a width of 32 NV)
+// into memory in operand order: [r][block s of 32 columns][lane][8], so that a
+// later kernel's lane reads its eight column elements of row l16 as one 16-byte
+// piece and a wave 1 KB in one go, with rows or columns as the product's rows
+// alike. The bf16 tile is 512 consecutive bytes. (Row by row instead, 32 bytes
+// per row and wave: local kernel 362 us against 305, reverse scan 374 against 365.)
+__device__ __forceinline__ void op_st(bf16* p, int r, int cb, int nv, uint2 x) {  // x: packed accumulator
+  const int lane = threadIdx.x & 63, g = lane >> 4, Q = (lane >> 2) & 3, q = lane & 3;
+  bf16* d = p + (r * nv + (cb >> 1)) * kFragElems;
+  *reinterpret_cast<uint2*>(d + (uint32_t)(((2 * (cb & 1) + (Q >> 1)) * 16 + 4 * g + q) * 8 + 4 * (Q & 1))) =
+      quad_transpose(x);
+}
+__device__ __forceinline__ void op_st(float* p, int r, int cb, int nv, const f32x4& x) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  float* d = p + (r * nv + (cb >> 1)) * kFragElems;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    d[(uint32_t)(((2 * (cb & 1) + (l16 >> 3)) * 16 + 4 * g + e) * 8 + (l16 & 7))] = x[e];
+}
+template <typename T>
+__device__ __forceinline__ void op_ld(Op8<T>& o, const T* p, int r, int s, int nv) {
+  ld_op(o, p + ((r * nv + s) * 64 + (threadIdx.x & 63)) * 8);
+}
+
 // sum over the 16 lanes that hold one accumulator row (rotations inside the
 // row: no LDS), in every lane
 template <int M>
 __device__ __forceinline__ float add_ror(float x) {
   return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + M,
-                                                                   0xF, 0xF, false));
+                                                                   0xF, 0xF, true));
 }
 __device__ __forceinline__ float row16_sum(float x) {
   return add_ror<8>(add_ror<4>(add_ror<2>(add_ror<1>(x))));
@@ -547,11 +572,14 @@ struct GdnLayout {
   float* scal;   // [chunk * HV + hv][kGdnScal][64]
   T* frag;       // [..][GdnWs<T>::fwd], or for the backward [..][GdnWs<T>::bwd]: M, P
   T* fragT;      // [..][GdnWs<T>::bwd]: M^T, P^T
-  T* S0;         // [..][K][V]
+  T* S0;         // [..][K][V] in operand order (op_st), as the next three
   T* Y;          // [..][64][V]
   T* dS;         // [..][K][V]
   T* D;          // [..][64][V]
-  float* tok;    // [..][V / 16][64]: <o, dO> of the columns, then their share of dg
+  float* tokf;   // [..][V / 16][64]: the tokens' scalars from the forward run, per 16 columns
+  float* tokr;   // [..][V / 16][64]: those from the reverse scan
+  float* dgc;    // [..][64]: sum of the scalars from a token to its chunk's end
+  double* tot;   // [..]: of the whole chunk
   float* end;    // [N * HV][V / 16]: <S_T, dS_T> of the columns
   float* par;    // [..][2]
   size_t bytes;
@@ -569,14 +597,18 @@ struct GdnLayout {
     scal = reinterpret_cast<float*>(take(n * kGdnScal * kC * sizeof(float)));
     frag = reinterpret_cast<T*>(take(n * (bwd ? GdnWs<T>::bwd : GdnWs<T>::fwd) * sizeof(T)));
     fragT = S0 = Y = dS = D = nullptr;
-    tok = end = par = nullptr;
+    tokf = tokr = dgc = end = par = nullptr;
+    tot = nullptr;
     if (bwd) {
       fragT = reinterpret_cast<T*>(take(n * GdnWs<T>::bwd * sizeof(T)));
       S0 = reinterpret_cast<T*>(take(n * d.K * d.V * sizeof(T)));
       Y = reinterpret_cast<T*>(take(n * kC * d.V * sizeof(T)));
       dS = reinterpret_cast<T*>(take(n * d.K * d.V * sizeof(T)));
       D = reinterpret_cast<T*>(take(n * kC * d.V * sizeof(T)));
-      tok = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
+      tokf = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
+      tokr = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
+      dgc = reinterpret_cast<float*>(take(n * kC * sizeof(float)));
+      tot = reinterpret_cast<double*>(take(n * sizeof(double)));
       end = reinterpret_cast<float*>(take((size_t)d.N * d.HV * (d.V / 16) * sizeof(float)));
       par = reinterpret_cast<float*>(take(n * 2 * sizeof(float)));
     }

@@ -574,16 +574,15 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
 #pragma unroll
         for (int t = 0; t < 4; ++t) tile_ld(dr[t], dO + vrow(it), HV * V, perm_row4(t, g), col0, tokens(it));
       }
-      // S0 (its high part) row by row, and Y
-      bf16* s0 = ws_S0 + chunk(c) * K * V;
+      // S0 (its high part) and Y
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const uint4 w = __builtin_bit_cast(uint4, sb[r >> 1].hi);
-        const uint2 y = quad_transpose((r & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y));
-        *reinterpret_cast<uint2*>(s0 + (uint32_t)((perm_row4(r, g) + (l16 & 3)) * V + col0 + 4 * (l16 >> 2))) = y;
+        op_st(ws_S0 + chunk(c) * K * V, r, col0 >> 4, V / 32,
+              (r & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y));
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) tile_st(ws_Y + chunk(c) * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+      for (int t = 0; t < 4; ++t) op_st(ws_Y + chunk(c) * kC * V, t, col0 >> 4, V / 32, pack4(x[t]));
     }
     // O = e^G q~ S0 + P Delta, Delta = b Y
     Op8<bf16> qa[2][4], pf[L_::PT][6];
@@ -721,7 +720,7 @@ gdn_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, cons
     const float el = ws_scal[cc * (kGdnScal * kC) + kSl * kC];
     if constexpr (BWD) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) tile_st(ws_S0 + cc * K * V, V, perm_row4(r, g), col0, K, S[r]);
+      for (int r = 0; r < RT; ++r) op_st(ws_S0 + cc * K * V, r, col0 >> 4, V / 32, S[r]);
     }
     lds_dma_wait();
     __syncthreads();
@@ -764,7 +763,7 @@ gdn_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, cons
       }
     if constexpr (BWD) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) tile_st(ws_Y + cc * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+      for (int t = 0; t < 4; ++t) op_st(ws_Y + cc * kC * V, t, col0 >> 4, V / 32, x[t]);
     }
     Op8s<float> eb[2], db[2];
 #pragma unroll
@@ -849,7 +848,7 @@ static hipError_t scan_t(const kda_dims& d, const GdnCall& c, const GdnLayout<bf
   hipLaunchKernelGGL((gdn_scan_kernel<K, V, NP, BWD>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
                      dim3(128 * NP), lds, s, (const bf16*)c.q, (const bf16*)c.k, (const bf16*)c.v, c.h0, c.cu,
                      w.table, d.N, d.T, d.H, d.HV, w.scal, w.frag, c.ht != nullptr, (bf16*)c.o, c.ht,
-                     (const bf16*)c.dO, c.dht, w.S0, w.Y, w.tok, w.end);
+                     (const bf16*)c.dO, c.dht, w.S0, w.Y, w.tokf, w.end);
   return hipGetLastError();
 }
 template <int K, int V, int NP, bool BWD>

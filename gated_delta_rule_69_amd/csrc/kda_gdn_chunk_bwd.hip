@@ -3,8 +3,9 @@
 //
 //   gdn_rev_scan_kernel   one wave per 16 columns of one (sequence, value head)
 //                         state gradient, walking the chunks backwards; writes
-//                         dv, the columns' share of dg, and per chunk dS (at the
-//                         chunk's end) and D.
+//                         dv, its part of the tokens' scalars, and per chunk dS
+//                         (at the chunk's end) and D.
+//   gdn_tok_kernel        the tokens' scalars of a chunk, summed to its end.
 //   gdn_local_kernel      one workgroup per (chunk, q/k head), wave w owning
 //                         token tile w: dq, dk (summed over the head's value
 //                         heads) and dbeta from the chunk's S0, Y, dS and D, and
@@ -43,8 +44,8 @@ namespace kda {
 //   dS = e^{G_last} dS + Z - (e^G k)^T b D
 // with p = P^T dO (P strictly lower) and Z = (e^G q~)^T dO from the side wave,
 // which works a chunk ahead on these (they do not depend on dS) and a chunk
-// behind on what leaves: dS, D and dv = b D in memory, and the columns' share
-// of dg. It also issues the transfers of left operands into LDS. Two barriers
+// behind on what leaves: dS, D and dv = b D in memory, and the columns' part
+// of the tokens' scalars. It also issues the transfers of left operands into LDS. Two barriers
 // per chunk: at its top (operands, p and Z in LDS), and after the state wave
 // has taken p and Z and the side wave the previous chunk's dS and D'; the side
 // wave does its own products behind that one, where the state wave does not
@@ -80,9 +81,8 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
                     const int* __restrict__ table, int N, int T_, int H, int HV,
                     const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag, bf16* __restrict__ dv,
                     float* __restrict__ dh0, bf16* __restrict__ ws_dS, bf16* __restrict__ ws_D,
-                    float* __restrict__ ws_tok, const float* __restrict__ ws_end) {
+                    float* __restrict__ ws_tok) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  __shared__ __attribute__((aligned(16))) float s_tok[NP][kC];
   using L_ = GdnRevLds<K, NP>;
   using TT = TokTile<bf16, K>;
   constexpr int NK = K / 32, RT = K / 16, BV = 16 * NP, NVB = V / BV;
@@ -346,8 +346,6 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
 #pragma unroll
     for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(xZ + (r * 64 + lane) * 16) = Z[r];
   };
-  // sum over the tokens behind a chunk of the tokens' scalars, these columns
-  double behind = dht ? (double)ws_end[((size_t)ch.n * HV + hv) * (V / 16) + (col0 >> 4)] : 0.;
   // prologue: operands, p and Z of the last chunk
   fetch_s(nc - 1, 0);
   fetch_o(nc - 1);
@@ -358,7 +356,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
   ahead(nc - 1);
   put();
   TileRaw<bf16> vb[4], db[4];  // v and dO of the chunk behind, fetched a round early
-  float bw[4][4], pw[4][4], od = 0.f;
+  float bw[4][4], pw[4][4];
   auto fetch_b = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -368,13 +366,12 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
       lds4(f + kSb * kC + perm_row4(t, g), bw[t]);
       lds4(f + kSp * kC + perm_row4(t, g), pw[t]);
     }
-    od = ws_tok[(chunk(c) * (V / 16) + (col0 >> 4)) * kC + lane];
   };
   for (int c = nc - 1, buf = 0; c >= -1; --c, buf ^= 1) {
     const int cb = c + 1;  // the chunk behind
     // behind the previous round's transfers, if that round had a chunk behind:
-    // its stores (dS RT, D 4, share of dg 1)
-    if (cb + 1 < nc) lds_dma_wait_but<RT + 5>();
+    // its stores (dS RT, D 4, scalars 4)
+    if (cb + 1 < nc) lds_dma_wait_but<RT + 8>();
     else lds_dma_wait();
     __syncthreads();
 #pragma unroll
@@ -390,7 +387,6 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
         }
       }
     }
-    if (cb < nc) settle(od);
     if (c > 0) fetch_s(c - 1, buf ^ 1);
     if (c > 1) fetch_o(c - 2);
     uint4 sh[NK];
@@ -403,7 +399,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     }
     __syncthreads();
     f32x4 dd[4];
-    double y = 0.;
+    float4 sv[4];
     if (cb < nc) {  // the values of the chunk behind; their stores come last
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -415,19 +411,8 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
           x[t][e] = fmaf(pw[t][e], dt[e], x[t][e]);
           dd[t][e] = x[t][e] * bw[t][e];
         }
-        if (l16 == 0)
-          *reinterpret_cast<float4*>(&s_tok[pair][perm_row4(t, g)]) = make_float4(z[0], z[1], z[2], z[3]);
+        sv[t] = make_float4(z[0], z[1], z[2], z[3]);
       }
-      // the columns' share of dg: lane = token, sums from the sequence's end
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      y = lane < tokens(cb) ? (double)od - (double)s_tok[pair][lane] : 0.;
-#pragma unroll
-      for (int i = 1; i < 64; i <<= 1) {
-        const double z = __shfl_down(y, i);
-        if (lane + i < 64) y += z;
-      }
-      y += behind;
-      behind = __shfl(y, 0);
     }
     stage();
     if (c >= 0) fetch_b(c);
@@ -437,21 +422,49 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     }
     asm volatile("" ::: "memory");  // every load above, the stores below
     if (cb < nc) {
-      bf16* ds = ws_dS + chunk(cb) * K * V;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const uint2 w = quad_transpose((r & 1) ? make_uint2(sh[r >> 1].z, sh[r >> 1].w)
-                                               : make_uint2(sh[r >> 1].x, sh[r >> 1].y));
-        *reinterpret_cast<uint2*>(ds + (uint32_t)((perm_row4(r, g) + (l16 & 3)) * V + col0 + 4 * (l16 >> 2))) = w;
-      }
+      for (int r = 0; r < RT; ++r)
+        op_st(ws_dS + chunk(cb) * K * V, r, col0 >> 4, V / 32,
+              (r & 1) ? make_uint2(sh[r >> 1].z, sh[r >> 1].w) : make_uint2(sh[r >> 1].x, sh[r >> 1].y));
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        tile_st(ws_D + chunk(cb) * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+        op_st(ws_D + chunk(cb) * kC * V, t, col0 >> 4, V / 32, pack4(x[t]));
         tile_st(dv + vrow(cb), HV * V, perm_row4(t, g), col0, tokens(cb), dd[t]);
       }
-      ws_tok[(chunk(cb) * (V / 16) + (col0 >> 4)) * kC + lane] = (float)y;
+      float* tk = ws_tok + (chunk(cb) * (V / 16) + (col0 >> 4)) * kC;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (l16 == 0) *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = sv[t];
     }
   }
+}
+
+// Per (chunk, value head), one wave: the tokens' scalars over all columns,
+// summed from each token to the chunk's end, and the chunk's total.
+template <int V>
+__global__ void __launch_bounds__(256)
+gdn_tok_kernel(const int32_t* __restrict__ cu, const int* __restrict__ table, int N, int T_, int HV, int64_t n,
+               const float* __restrict__ tokf, const float* __restrict__ tokr, float* __restrict__ dgc,
+               double* __restrict__ tot) {
+  const int lane = threadIdx.x & 63;
+  const int64_t ch = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (ch >= n) return;
+  const ChunkGeo geo = chunk_geo((int)(ch / HV), cu, table, N, T_);
+  if (!geo.ok) return;
+  double y = 0.;
+#pragma unroll
+  for (int i = 0; i < V / 16; ++i) {
+    const size_t at = ((size_t)ch * (V / 16) + i) * kC + lane;
+    y += (double)tokf[at] - (double)tokr[at];
+  }
+  if (lane >= geo.L) y = 0.;
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) {
+    const double z = __shfl_down(y, i);
+    if (lane + i < 64) y += z;
+  }
+  dgc[ch * kC + lane] = (float)y;
+  if (lane == 0) tot[ch] = y;
 }
 
 // FP32: one wave per 16 columns, FP32 matrix cores, one operand buffer.
@@ -513,7 +526,7 @@ gdn_rev_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
       x[t] = p[t] = zero4();
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r) tile_st(ws_dS + cc * K * V, V, perm_row4(r, g), col0, K, S[r]);
+    for (int r = 0; r < RT; ++r) op_st(ws_dS + cc * K * V, r, col0 >> 4, V / 32, S[r]);
     lds_dma_wait();
     __syncthreads();
     const float el = sf[kSl * kC];
@@ -560,7 +573,7 @@ gdn_rev_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
         x[t] = mma8s(a, rb[s], x[t]);
       }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) tile_st(ws_D + cc * kC * V, V, perm_row4(t, g), col0, kC, x[t]);
+    for (int t = 0; t < 4; ++t) op_st(ws_D + cc * kC * V, t, col0 >> 4, V / 32, x[t]);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       f32x4 eq[2], ek[2];
@@ -619,7 +632,8 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
                  const int32_t* __restrict__ cu, const int* __restrict__ table, int N, int T_, int H,
                  int HV, int l2, int has_h0, float scale, const float* __restrict__ ws_scal,
                  const T* __restrict__ ws_S0, const T* __restrict__ ws_Y, const T* __restrict__ ws_dS,
-                 const T* __restrict__ ws_D, const float* __restrict__ ws_tok, T* __restrict__ dq, T* __restrict__ dk,
+                 const T* __restrict__ ws_D, const float* __restrict__ ws_dgc, const double* __restrict__ ws_tot,
+                 const float* __restrict__ ws_end, int has_dht, T* __restrict__ dq, T* __restrict__ dk,
                  T* __restrict__ dbeta, void* __restrict__ dgate, float* __restrict__ par) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   using TT = TokTile<T, K>;
@@ -668,8 +682,8 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
 #pragma unroll
     for (int s = 0; s < NV; ++s) {
       ld_op(od[s], dOb + (int64_t)min(own, L - 1) * HV * V + 32 * s + 8 * g);
-      ld_op(oD[s], Db + own * V + 32 * s + 8 * g);
-      ld_op(oY[s], Yb + own * V + 32 * s + 8 * g);
+      op_ld(oD[s], Db, wave, s, NV);
+      op_ld(oY[s], Yb, wave, s, NV);
     }
     float fk[4], fq[4], fe[4], fb[4], frq[4], frk[4];
     lds4(sc + kSk * kC + own4, fk);
@@ -724,7 +738,7 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
 #pragma unroll
           for (int u = 0; u < NV; ++u) {
             Op8<T> y;
-            ld_op(y, Yb + row * V + 32 * u + 8 * g);
+            op_ld(y, Yb, 2 * s + i, u, NV);
             w[i] = mma8(y, od[u], w[i]);
             z[i] = mma8(y, oD[u], z[i]);
           }
@@ -734,7 +748,7 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
           for (int u = 0; u < NV; ++u) {
             Op8<T> a, d;
             ld_op(a, dOb + (int64_t)min(row, L - 1) * HV * V + 32 * u + 8 * g);
-            ld_op(d, Db + row * V + 32 * u + 8 * g);
+            op_ld(d, Db, 2 * s + i, u, NV);
             w2[i] = mma8(a, oY[u], w2[i]);
             z2[i] = mma8(d, oY[u], z2[i]);
           }
@@ -777,13 +791,12 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
     const T* dSb = ws_dS + ch * K * V;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const int c = perm_row(r, l16);
       f32x4 a1 = zero4(), a2 = zero4(), a3 = zero4();
 #pragma unroll
       for (int s = 0; s < NV; ++s) {
         Op8<T> s0, ds;
-        ld_op(s0, S0b + (size_t)c * V + 32 * s + 8 * g);
-        ld_op(ds, dSb + (size_t)c * V + 32 * s + 8 * g);
+        op_ld(s0, S0b, r, s, NV);
+        op_ld(ds, dSb, r, s, NV);
         a1 = mma8(od[s], s0, a1);
         a2 = mma8(oD[s], s0, a2);
         a3 = mma8(oY[s], ds, a3);
@@ -857,9 +870,14 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
         }
         dg = r + (c - c_own) + sc[kSl * kC] * ((sS[0] + sS[1]) + (sS[2] + sS[3]));
       } else {
-        const float* tk = ws_tok + ch * (V / 16) * kC + lane;
+        // tokens from this one to its chunk's end, the chunks behind, and the end itself
+        double y = 0.;
+        const int last = cu ? table[2 + geo.n] : (geo.n + 1) * ((T_ + kC - 1) / kC);  // end of the sequence's chunks
+        for (int c2 = j + 1 + lane; c2 < last; c2 += 64) y += ws_tot[(size_t)c2 * HV + hv];
+        if (has_dht && lane < V / 16) y += (double)ws_end[((size_t)geo.n * HV + hv) * (V / 16) + lane];
 #pragma unroll
-        for (int i = 0; i < V / 16; ++i) dg += tk[i * kC];
+        for (int d = 32; d; d >>= 1) y += __shfl_xor(y, d);
+        dg = (float)((double)ws_dgc[ch * kC + lane] + y);
       }
       // before a sequence's first token there is nothing to decay without a state
       if (geo.c == 0 && lane == 0 && !has_h0) dg = 0.f;
@@ -974,13 +992,13 @@ static hipError_t rev_t(const kda_dims& d, const void* q, const void* k, const v
                         const float* dht, const int32_t* cu, const GdnLayout<bf16>& w, void* dv, float* dh0,
                         hipStream_t s) {
   constexpr size_t lds = GdnRevLds<K, NP>::total;
-  static_assert(lds + NP * kC * sizeof(float) <= 160 * 1024, "LDS");
+  static_assert(lds <= 160 * 1024, "LDS");
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_rev_scan_kernel<K, V, NP>),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((gdn_rev_scan_kernel<K, V, NP>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
                      dim3(128 * NP), lds, s, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)dO, dht,
-                     cu, w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (bf16*)dv, dh0, w.dS, w.D, w.tok, w.end);
+                     cu, w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (bf16*)dv, dh0, w.dS, w.D, w.tokr);
   return hipGetLastError();
 }
 template <int K, int V, int NP>
@@ -1009,14 +1027,21 @@ static hipError_t gdn_bwd_kv(const kda_dims& d, const void* q, const void* k, co
   if (d.N > 0) e = rev_t<K, V, 2>(d, q, k, v, dO, dht, cu, w, dv, dh0, s);
   if (e != hipSuccess) return e;
   if (d.N > 0 && mc > 0) {
+    if constexpr (GdnWs<T>::kScanGate) {
+      const int64_t n = mc * d.HV;
+      hipLaunchKernelGGL((gdn_tok_kernel<V>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, s, cu, w.table, d.N, d.T,
+                         d.HV, n, w.tokf, w.tokr, w.dgc, w.tot);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
     constexpr size_t lds = 2 * TokTile<T, K>::bytes;
     e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_local_kernel<T, K, V>),
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gdn_local_kernel<T, K, V>), dim3((unsigned)(mc * d.H)), dim3(256), lds, s,
                        (const T*)q, (const T*)k, (const T*)dO, gate, cu, w.table, d.N, d.T, d.H, d.HV, l2,
-                       h0 != nullptr ? 1 : 0, 1.0f / sqrtf((float)K), w.scal, w.S0, w.Y, w.dS, w.D, w.tok,
-                       (T*)dq, (T*)dk, (T*)dbeta, dgate, w.par);
+                       h0 != nullptr ? 1 : 0, 1.0f / sqrtf((float)K), w.scal, w.S0, w.Y, w.dS, w.D, w.dgc, w.tot, w.end,
+                       dht != nullptr ? 1 : 0, (T*)dq, (T*)dk, (T*)dbeta, dgate, w.par);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
