@@ -257,9 +257,10 @@ __device__ __forceinline__ f32x4 unpack4(uint2 r) {
 // element (r, c) at p + r * stride + c. Rows from `rows` on are not written; as
 // loads they repeat the last row (unconditional loads: under a lane-dependent
 // branch each would be waited for at the branch's join), and what they feed is
-// multiplied by row factors that are zero there. bf16: p 8-byte aligned, stride and col0 multiples of 4. p is uniform
-// in the wave and 64 rows span less than 2^31 bytes (checked by the entry
-// points), so a lane's address is a scalar base and a 32-bit offset.
+// multiplied by row factors that are zero there. bf16: p 8-byte aligned, stride
+// and col0 multiples of 4. p is uniform in the wave and 64 rows span less than
+// 2^31 bytes (checked by the entry points), so a lane's address is a scalar
+// base and a 32-bit offset.
 template <typename T>
 struct TileRaw;
 template <>

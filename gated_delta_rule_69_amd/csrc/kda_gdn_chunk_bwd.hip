@@ -38,18 +38,18 @@
 namespace kda {
 
 // ------------------------------------------------------------------ reverse scan
-// bf16. Two waves per 16 columns, as in the forward scan. The state wave keeps
-// dS and walks
+// bf16. Three waves per 16 columns. The state wave keeps dS and walks
 //   x = e^{G_last - G} k dS + p,  D' = x - M^T b (x + P_ii dO),  D = D' + P_ii dO,
 //   dS = e^{G_last} dS + Z - (e^G k)^T b D
-// with p = P^T dO (P strictly lower) and Z = (e^G q~)^T dO from the side wave,
-// which works a chunk ahead on these (they do not depend on dS) and a chunk
-// behind on what leaves: dS, D and dv = b D in memory, and the columns' part
-// of the tokens' scalars. It also issues the transfers of left operands into LDS. Two barriers
-// per chunk: at its top (operands, p and Z in LDS), and after the state wave
-// has taken p and Z and the side wave the previous chunk's dS and D'; the side
-// wave does its own products behind that one, where the state wave does not
-// wait for them.
+// with p = P^T dO (P strictly lower) and Z = (e^G q~)^T dO, which do not depend
+// on dS: the ahead wave forms them a chunk early, and issues the transfers of
+// left operands into LDS. The behind wave follows a chunk late with what
+// leaves: dS, D and dv = b D in memory, and the columns' part of the tokens'
+// scalars. (One side wave doing both was the step's longest: 373 us at 64
+// chains.) Two barriers per chunk: at its top (operands, p and Z in LDS), and
+// after the state wave has taken p and Z and the behind wave the previous
+// chunk's dS and D'. Of the workgroup's 4 NP waves NP leave at once: the state
+// waves then have a SIMD each, ahead and behind waves share the others.
 template <int K, int NP>
 struct GdnRevLds {
   static constexpr int NK = K / 32, RT = K / 16;
@@ -75,7 +75,7 @@ __device__ __forceinline__ void mma_up(const Op8<bf16> (&a)[6], const bf16x8 (&b
 }
 
 template <int K, int V, int NP>
-__global__ void __launch_bounds__(NP * 128)
+__global__ void __launch_bounds__(NP * 256)
 gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
                     const bf16* __restrict__ dO, const float* __restrict__ dht, const int32_t* __restrict__ cu,
                     const int* __restrict__ table, int N, int T_, int H, int HV,
@@ -88,13 +88,14 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
   constexpr int NK = K / 32, RT = K / 16, BV = 16 * NP, NVB = V / BV;
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pair = wave % NP;
+  const int pair = wave % NP, role = wave / NP;  // 0 state, 1 ahead, 3 behind
+  if (role == 2) return;
   const GdnChain ch = gdn_chain(NVB, cu, table, N, T_, H, HV);
   if (!ch.ok) return;
   const int col0 = ch.vb * BV + 16 * pair, hv = ch.hv, len = ch.len;
   const size_t st = ((size_t)ch.n * HV + hv) * (size_t)K * V;
   if (len <= 0) {
-    if (dh0 && wave < NP) gdn_pass(dht, dh0, st, K, V, col0);
+    if (dh0 && role == 0) gdn_pass(dht, dh0, st, K, V, col0);
     return;
   }
   const int nc = (len + kC - 1) / kC;
@@ -105,7 +106,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
   char* xp = xch + L_::xS + L_::xD;
   char* xZ = xp + L_::xp;
 
-  if (wave < NP) {
+  if (role == 0) {
     f32x4 S[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -247,7 +248,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
       }
     }
     __builtin_amdgcn_s_setprio(0);
-    __syncthreads();  // the side wave's last chunk
+    __syncthreads();  // the behind wave's last chunk
     __syncthreads();
     if (dh0) {
 #pragma unroll
@@ -259,102 +260,110 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     return;
   }
 
-  // ---- side wave
-  const uint32_t lds = lds_addr(smem);
-  const TokDma<bf16, K, NP> tok((uint32_t)(H * K * sizeof(bf16)), pair);
-  auto fetch_s = [&](int c, int buf) __attribute__((always_inline)) {
-    const uint32_t b = lds + buf * L_::sbuf;
-    tok.go(b, k + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
-    dma_flat<2 * L_::tri, NP>(b + L_::sM, ws_frag + chunk(c) * GdnWs<bf16>::bwd, pair);
-    dma_flat<L_::scal, NP>(b + L_::sF, ws_scal + chunk(c) * (kGdnScal * kC), pair);
-    dma_flat<L_::scal, NP>(b + L_::sE, ws_scal + chunk(c) * (kGdnScal * kC) + kSe * kC, pair);
-  };
-  auto fetch_o = [&](int c) __attribute__((always_inline)) {
-    const uint32_t b = lds + L_::at_o + (c & 1) * L_::obuf;
-    tok.go(b, q + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
-    dma_flat<2 * L_::tri, NP>(b + L_::oP, ws_frag + chunk(c) * GdnWs<bf16>::bwd + 2 * kTriElems, pair);
-    dma_flat<L_::scal, NP>(b + L_::oF, ws_scal + chunk(c) * (kGdnScal * kC) + kSb * kC, pair);
-  };
-  TileRaw<bf16> dn[4];  // dO of the chunk ahead
-  auto fetch_dn = [&](int c) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) tile_ld(dn[t], dO + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
-  };
-  f32x4 p[4], Z[RT];
-  auto ahead = [&](int c) __attribute__((always_inline)) {  // p and Z of chunk c
-    const char* ob = smem + L_::at_o + (c & 1) * L_::obuf;
-    const bf16* sP = reinterpret_cast<const bf16*>(ob + L_::oP);
-    const float* of = reinterpret_cast<const float*>(ob + L_::oF);  // from slot kSb on
-    Op8<bf16> pf[2][6];
-#pragma unroll
-    for (int f = 0; f < 6; ++f)
-#pragma unroll
-      for (int pt = 0; pt < 2; ++pt) ld_op(pf[pt][f], sP + pt * kTriElems + f * kFragElems + lane * 8);
-    Op8<bf16> dop[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) tile_op(dop[s], dn[2 * s], dn[2 * s + 1]);
-    Op8s<bf16> qb[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      f32x4 d[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 w = __builtin_bit_cast(uint4, dop[s].v);
-        d[i] = unpack4(i ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y));
-        float f[4];
-        lds4(of + (kSq - kSb) * kC + perm_row4(2 * s + i, g), f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) d[i][e] *= f[e];
-      }
-      make_op(qb[s], d[0], d[1]);
-    }
-    if (c > 0) fetch_dn(c - 1);
-    stage();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) p[t] = zero4();
-    const bf16x8 dd[2] = {dop[0].v, dop[1].v};
-    mma_up(pf[1], dd, p);
-    mma_up(pf[0], dd, p);
-    Op8<bf16> qc[RT][2];
-    auto read_qc = [&](int r) __attribute__((always_inline)) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) TT::cols(qc[r][s], ob, r, s);
+  if (role == 1) {
+    const uint32_t lds = lds_addr(smem);
+    const TokDma<bf16, K, NP> tok((uint32_t)(H * K * sizeof(bf16)), pair);
+    auto fetch_s = [&](int c, int buf) __attribute__((always_inline)) {
+      const uint32_t b = lds + buf * L_::sbuf;
+      tok.go(b, k + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
+      dma_flat<2 * L_::tri, NP>(b + L_::sM, ws_frag + chunk(c) * GdnWs<bf16>::bwd, pair);
+      dma_flat<L_::scal, NP>(b + L_::sF, ws_scal + chunk(c) * (kGdnScal * kC), pair);
+      dma_flat<L_::scal, NP>(b + L_::sE, ws_scal + chunk(c) * (kGdnScal * kC) + kSe * kC, pair);
     };
-    read_qc(0);
-    read_qc(1);
+    auto fetch_o = [&](int c) __attribute__((always_inline)) {
+      const uint32_t b = lds + L_::at_o + (c & 1) * L_::obuf;
+      tok.go(b, q + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
+      dma_flat<2 * L_::tri, NP>(b + L_::oP, ws_frag + chunk(c) * GdnWs<bf16>::bwd + 2 * kTriElems, pair);
+      dma_flat<L_::scal, NP>(b + L_::oF, ws_scal + chunk(c) * (kGdnScal * kC) + kSb * kC, pair);
+    };
+    TileRaw<bf16> dn[4];  // dO of the chunk ahead
+    auto fetch_dn = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < RT; r += 2) {
-      stage();
-      if (r + 2 < RT) {
-        read_qc(r + 2);
-        read_qc(r + 3);
-      }
-      stage();
-      Z[r] = Z[r + 1] = zero4();
+      for (int t = 0; t < 4; ++t) tile_ld(dn[t], dO + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
+    };
+    auto ahead = [&](int c) __attribute__((always_inline)) {  // p and Z of chunk c into LDS
+      const char* ob = smem + L_::at_o + (c & 1) * L_::obuf;
+      const bf16* sP = reinterpret_cast<const bf16*>(ob + L_::oP);
+      const float* of = reinterpret_cast<const float*>(ob + L_::oF);  // from slot kSb on
+      Op8<bf16> pf[2][6];
+#pragma unroll
+      for (int f = 0; f < 6; ++f)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) ld_op(pf[pt][f], sP + pt * kTriElems + f * kFragElems + lane * 8);
+      Op8<bf16> dop[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) tile_op(dop[s], dn[2 * s], dn[2 * s + 1]);
+      Op8s<bf16> qb[2];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        Z[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r][s].v, qb[s].lo, Z[r], 0, 0, 0);
-        Z[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r + 1][s].v, qb[s].lo, Z[r + 1], 0, 0, 0);
-        Z[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r][s].v, qb[s].hi, Z[r], 0, 0, 0);
-        Z[r + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r + 1][s].v, qb[s].hi, Z[r + 1], 0, 0, 0);
+        f32x4 d[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 w = __builtin_bit_cast(uint4, dop[s].v);
+          d[i] = unpack4(i ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y));
+          float f[4];
+          lds4(of + (kSq - kSb) * kC + perm_row4(2 * s + i, g), f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[i][e] *= f[e];
+        }
+        make_op(qb[s], d[0], d[1]);
       }
+      if (c > 0) fetch_dn(c - 1);
+      Op8<bf16> qc[RT][2];
+      auto read_qc = [&](int r) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) TT::cols(qc[r][s], ob, r, s);
+      };
+      read_qc(0);
+      read_qc(1);
+      stage();
+      f32x4 p[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) p[t] = zero4();
+      const bf16x8 dd[2] = {dop[0].v, dop[1].v};
+      mma_up(pf[1], dd, p);
+      mma_up(pf[0], dd, p);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(xp + (t * 64 + lane) * 16) = p[t];
+#pragma unroll
+      for (int r = 0; r < RT; r += 2) {
+        stage();
+        if (r + 2 < RT) {
+          read_qc(r + 2);
+          read_qc(r + 3);
+        }
+        stage();
+        f32x4 z0 = zero4(), z1 = zero4();
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          z0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r][s].v, qb[s].lo, z0, 0, 0, 0);
+          z1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r + 1][s].v, qb[s].lo, z1, 0, 0, 0);
+          z0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r][s].v, qb[s].hi, z0, 0, 0, 0);
+          z1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qc[r + 1][s].v, qb[s].hi, z1, 0, 0, 0);
+        }
+        *reinterpret_cast<f32x4*>(xZ + (r * 64 + lane) * 16) = z0;
+        *reinterpret_cast<f32x4*>(xZ + ((r + 1) * 64 + lane) * 16) = z1;
+      }
+    };
+    fetch_s(nc - 1, 0);
+    fetch_o(nc - 1);
+    if (nc > 1) fetch_o(nc - 2);
+    fetch_dn(nc - 1);
+    lds_dma_wait();
+    __syncthreads();
+    ahead(nc - 1);
+    for (int c = nc - 1, buf = 0; c >= -1; --c, buf ^= 1) {
+      lds_dma_wait();
+      __syncthreads();
+      if (c > 0) fetch_s(c - 1, buf ^ 1);
+      if (c > 1) fetch_o(c - 2);
+      __syncthreads();
+      if (c > 0) ahead(c - 1);
     }
-  };
-  auto put = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) *reinterpret_cast<f32x4*>(xp + (t * 64 + lane) * 16) = p[t];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(xZ + (r * 64 + lane) * 16) = Z[r];
-  };
-  // prologue: operands, p and Z of the last chunk
-  fetch_s(nc - 1, 0);
-  fetch_o(nc - 1);
-  if (nc > 1) fetch_o(nc - 2);
-  fetch_dn(nc - 1);
-  lds_dma_wait();
-  __syncthreads();
-  ahead(nc - 1);
-  put();
+    return;
+  }
+
+  // ---- behind wave
   TileRaw<bf16> vb[4], db[4];  // v and dO of the chunk behind, fetched a round early
   float bw[4][4], pw[4][4];
   auto fetch_b = [&](int c) __attribute__((always_inline)) {
@@ -367,28 +376,11 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
       lds4(f + kSp * kC + perm_row4(t, g), pw[t]);
     }
   };
-  for (int c = nc - 1, buf = 0; c >= -1; --c, buf ^= 1) {
+  fetch_b(nc - 1);
+  __syncthreads();  // the last chunk's operands
+  for (int c = nc - 1; c >= -1; --c) {
     const int cb = c + 1;  // the chunk behind
-    // behind the previous round's transfers, if that round had a chunk behind:
-    // its stores (dS RT, D 4, scalars 4)
-    if (cb + 1 < nc) lds_dma_wait_but<RT + 8>();
-    else lds_dma_wait();
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (c > 0) settle(dn[t].r);
-      if (cb < nc) {
-        settle(vb[t].r);
-        settle(db[t].r);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          settle(bw[t][e]);
-          settle(pw[t][e]);
-        }
-      }
-    }
-    if (c > 0) fetch_s(c - 1, buf ^ 1);
-    if (c > 1) fetch_o(c - 2);
     uint4 sh[NK];
     f32x4 x[4];
     if (cb < nc) {
@@ -398,47 +390,41 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
       for (int t = 0; t < 4; ++t) x[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + (t * 64 + lane) * 16);
     }
     __syncthreads();
+    if (cb >= nc) continue;
     f32x4 dd[4];
     float4 sv[4];
-    if (cb < nc) {  // the values of the chunk behind; their stores come last
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const f32x4 vt = tile_get(vb[t]), dt = tile_get(db[t]);
-        float z[4];
+    for (int t = 0; t < 4; ++t) {
+      const f32x4 vt = tile_get(vb[t]), dt = tile_get(db[t]);
+      float z[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z[e] = row16_sum(bw[t][e] * x[t][e] * vt[e]);
-          x[t][e] = fmaf(pw[t][e], dt[e], x[t][e]);
-          dd[t][e] = x[t][e] * bw[t][e];
-        }
-        sv[t] = make_float4(z[0], z[1], z[2], z[3]);
+      for (int e = 0; e < 4; ++e) {
+        z[e] = row16_sum(bw[t][e] * x[t][e] * vt[e]);
+        x[t][e] = fmaf(pw[t][e], dt[e], x[t][e]);
+        dd[t][e] = x[t][e] * bw[t][e];
       }
+      sv[t] = make_float4(z[0], z[1], z[2], z[3]);
     }
     stage();
     if (c >= 0) fetch_b(c);
-    if (c > 0) {
-      ahead(c - 1);
-      put();
+    stage();
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      op_st(ws_dS + chunk(cb) * K * V, r, col0 >> 4, V / 32,
+            (r & 1) ? make_uint2(sh[r >> 1].z, sh[r >> 1].w) : make_uint2(sh[r >> 1].x, sh[r >> 1].y));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      op_st(ws_D + chunk(cb) * kC * V, t, col0 >> 4, V / 32, pack4(x[t]));
+      tile_st(dv + vrow(cb), HV * V, perm_row4(t, g), col0, tokens(cb), dd[t]);
     }
-    asm volatile("" ::: "memory");  // every load above, the stores below
-    if (cb < nc) {
+    float* tk = ws_tok + (chunk(cb) * (V / 16) + (col0 >> 4)) * kC;
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        op_st(ws_dS + chunk(cb) * K * V, r, col0 >> 4, V / 32,
-              (r & 1) ? make_uint2(sh[r >> 1].z, sh[r >> 1].w) : make_uint2(sh[r >> 1].x, sh[r >> 1].y));
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        op_st(ws_D + chunk(cb) * kC * V, t, col0 >> 4, V / 32, pack4(x[t]));
-        tile_st(dv + vrow(cb), HV * V, perm_row4(t, g), col0, tokens(cb), dd[t]);
-      }
-      float* tk = ws_tok + (chunk(cb) * (V / 16) + (col0 >> 4)) * kC;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (l16 == 0) *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = sv[t];
-    }
+    for (int t = 0; t < 4; ++t)
+      if (l16 == 0) *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = sv[t];
   }
 }
 
+// FP32: one wave per 16 columns, FP32 matrix cores, one operand buffer.
 // Per (chunk, value head), one wave: the tokens' scalars over all columns,
 // summed from each token to the chunk's end, and the chunk's total.
 template <int V>
@@ -997,7 +983,7 @@ static hipError_t rev_t(const kda_dims& d, const void* q, const void* k, const v
                                      hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((gdn_rev_scan_kernel<K, V, NP>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
-                     dim3(128 * NP), lds, s, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)dO, dht,
+                     dim3(256 * NP), lds, s, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)dO, dht,
                      cu, w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (bf16*)dv, dh0, w.dS, w.D, w.tokr);
   return hipGetLastError();
 }
