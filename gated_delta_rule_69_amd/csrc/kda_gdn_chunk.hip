@@ -278,7 +278,8 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
 //
 // BWD: the backward's run over the forward. S0 and Y are kept instead of O, and
 // dO comes in: o' is formed in full precision (S0 and P split as well; P is
-// strictly lower) for the tokens' scalars of the gate's gradient.
+// strictly lower) for the tokens' scalars of the gate's gradient. A third wave
+// per pair stores S0 and Y (of 4 NP waves, NP leave at once).
 template <int K, int NP, bool BWD>
 struct GdnScanLds {
   static constexpr int NK = K / 32, PT = BWD ? 2 : 1;
@@ -294,7 +295,7 @@ struct GdnScanLds {
 };
 
 template <int K, int V, int NP, bool BWD>
-__global__ void __launch_bounds__(NP * 128, BWD ? 1 : 2)  // 2: 256 registers, none of them accumulation-only
+__global__ void __launch_bounds__(NP * (BWD ? 256 : 128), 2)  // 2: 256 registers, none of them accumulation-only
 gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
                 const float* h0, const int32_t* __restrict__ cu, const int* __restrict__ table, int N,
                 int T_, int H, int HV, const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag,
@@ -308,8 +309,9 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
   constexpr size_t kFrag = BWD ? GdnWs<bf16>::bwd : GdnWs<bf16>::fwd;
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pair = wave % NP;
-  const bool state_wave = wave < NP;
+  const int pair = wave % NP, role = wave / NP;  // 0 state, 1 output, 3 store
+  const bool state_wave = role == 0;
+  if (role == 2) return;
   const GdnChain ch = gdn_chain(NVB, cu, table, N, T_, H, HV);
   if (!ch.ok) return;
   const int col0 = ch.vb * BV + 16 * pair, hv = ch.hv, len = ch.len;
@@ -509,6 +511,32 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
     return;
   }
 
+  if constexpr (BWD) {
+    if (role == 3) {  // S0 (its high part) and Y of the chunk behind
+      __syncthreads();
+      for (int it = 0; it <= nc; ++it) {
+        __syncthreads();
+        uint4 s0[NK];
+        f32x4 x[4];
+        if (it > 0) {
+#pragma unroll
+          for (int s = 0; s < NK; ++s) s0[s] = *reinterpret_cast<const uint4*>(xch + (s * 64 + lane) * 16);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) x[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + (t * 64 + lane) * 16);
+        }
+        __syncthreads();
+        if (it == 0) continue;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          op_st(ws_S0 + chunk(it - 1) * K * V, r, col0 >> 4, V / 32,
+                (r & 1) ? make_uint2(s0[r >> 1].z, s0[r >> 1].w) : make_uint2(s0[r >> 1].x, s0[r >> 1].y));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) op_st(ws_Y + chunk(it - 1) * kC * V, t, col0 >> 4, V / 32, pack4(x[t]));
+      }
+      return;
+    }
+  }
+
   // ---- output wave
   const uint32_t lds = lds_addr(smem);
   const TokDma<bf16, K, NP> tok((uint32_t)(H * K * sizeof(bf16)), pair);
@@ -529,9 +557,8 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
   lds_dma_wait();
   __syncthreads();
   for (int it = 0; it <= nc; ++it) {
-    // behind the previous round's transfers: the stores of chunk it - 2, a full
-    // one (O: 4; BWD: S0 8 and Y 4)
-    if (it >= 2) lds_dma_wait_but<BWD ? RT + 4 : 4>();
+    // behind the previous round's transfers: the 4 stores of chunk it - 2, a full one
+    if (it >= 2) lds_dma_wait_but<4>();
     else lds_dma_wait();
     __syncthreads();
     if constexpr (BWD) {
@@ -574,15 +601,6 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
 #pragma unroll
         for (int t = 0; t < 4; ++t) tile_ld(dr[t], dO + vrow(it), HV * V, perm_row4(t, g), col0, tokens(it));
       }
-      // S0 (its high part) and Y
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const uint4 w = __builtin_bit_cast(uint4, sb[r >> 1].hi);
-        op_st(ws_S0 + chunk(c) * K * V, r, col0 >> 4, V / 32,
-              (r & 1) ? make_uint2(w.z, w.w) : make_uint2(w.x, w.y));
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) op_st(ws_Y + chunk(c) * kC * V, t, col0 >> 4, V / 32, pack4(x[t]));
     }
     // O = e^G q~ S0 + P Delta, Delta = b Y
     Op8<bf16> qa[2][4], pf[L_::PT][6];
@@ -846,7 +864,7 @@ static hipError_t scan_t(const kda_dims& d, const GdnCall& c, const GdnLayout<bf
   hipError_t e = set_lds(&gdn_scan_kernel<K, V, NP, BWD>, lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((gdn_scan_kernel<K, V, NP, BWD>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
-                     dim3(128 * NP), lds, s, (const bf16*)c.q, (const bf16*)c.k, (const bf16*)c.v, c.h0, c.cu,
+                     dim3((BWD ? 256 : 128) * NP), lds, s, (const bf16*)c.q, (const bf16*)c.k, (const bf16*)c.v, c.h0, c.cu,
                      w.table, d.N, d.T, d.H, d.HV, w.scal, w.frag, c.ht != nullptr, (bf16*)c.o, c.ht,
                      (const bf16*)c.dO, c.dht, w.S0, w.Y, w.tokf, w.end);
   return hipGetLastError();
