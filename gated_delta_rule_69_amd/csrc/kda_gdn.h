@@ -324,8 +324,8 @@ __device__ __forceinline__ void op_st(float* p, int r, int cb, int nv, const f32
     d[(uint32_t)(((2 * (cb & 1) + (l16 >> 3)) * 16 + 4 * g + e) * 8 + (l16 & 7))] = x[e];
 }
 template <typename T>
-__device__ __forceinline__ void op_ld(Op8<T>& o, const T* p, int r, int s, int nv) {
-  ld_op(o, p + ((r * nv + s) * 64 + (threadIdx.x & 63)) * 8);
+__device__ __forceinline__ void op_ld(Op8<T>& o, const T* p, int r, int s, int nv, int lane = threadIdx.x & 63) {
+  ld_op(o, p + ((r * nv + s) * 64 + lane) * 8);
 }
 
 // sum over the 16 lanes that hold one accumulator row (rotations inside the
@@ -354,8 +354,8 @@ struct TokTile {
   }
   static __device__ __forceinline__ int at(int r, int b) { return (r * kBlocks + (b ^ swz(r))) * 16; }
   // rows perm_row(t, l16), channels 32 s + 8 g .. + 7
-  static __device__ __forceinline__ void rows(Op8<T>& o, const char* s, int t, int ks) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, r = perm_row(t, lane & 15);
+  static __device__ __forceinline__ void rows(Op8<T>& o, const char* s, int t, int ks, int lane = threadIdx.x & 63) {
+    const int g = lane >> 4, r = perm_row(t, lane & 15);
     if constexpr (sizeof(T) == 2) {
       o.v = *reinterpret_cast<const bf16x8*>(s + at(r, 4 * ks + g));
     } else {
@@ -368,8 +368,8 @@ struct TokTile {
   // channels perm_row(t, l16), tokens 32 s + 8 g .. + 7 (the transposed read:
   // ds_read_b64_tr_b16 gives lane i of 16 column i of the four rows and four
   // 8-byte blocks the 16 lanes point at)
-  static __device__ __forceinline__ void cols(Op8<T>& o, const char* s, int t, int ks) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  static __device__ __forceinline__ void cols(Op8<T>& o, const char* s, int t, int ks, int lane = threadIdx.x & 63) {
+    const int g = lane >> 4, l16 = lane & 15;
     if constexpr (sizeof(T) == 2) {
       typedef short s16x4 __attribute__((ext_vector_type(4)));
       typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -390,8 +390,8 @@ struct TokTile {
     }
   }
   // accumulator-layout tile: rows perm_row4(tt, g) + e, channel perm_row(ct, l16)
-  static __device__ __forceinline__ f32x4 tile(const char* s, int tt, int ct) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  static __device__ __forceinline__ f32x4 tile(const char* s, int tt, int ct, int lane = threadIdx.x & 63) {
+    const int g = lane >> 4, l16 = lane & 15;
     if constexpr (sizeof(T) == 2) {
       const int r = perm_row4(tt, g) + (l16 & 3), b = 4 * (ct >> 1) + (l16 >> 2);
       const uint2 x = *reinterpret_cast<const uint2*>(s + at(r, b) + 8 * (ct & 1));
@@ -446,13 +446,18 @@ struct TokDma {
   uint32_t off[kPer], stride;
   int wave;
   // rows past `last` repeat it (their factors are zero)
-  __device__ __forceinline__ uint32_t unit(int n, int last) const {
-    const int u = 64 * (n * NW + wave) + (threadIdx.x & 63), r = u / TT::kBlocks;
+  __device__ __forceinline__ uint32_t unit(int n, int last, int lane = threadIdx.x & 63) const {
+    const int u = 64 * (n * NW + wave) + lane, r = u / TT::kBlocks;
     return min(r, last) * stride + 16 * ((u % TT::kBlocks) ^ TT::swz(r));
   }
   __device__ __forceinline__ TokDma(uint32_t stride_bytes, int w) : stride(stride_bytes), wave(w) {
 #pragma unroll
     for (int n = 0; n < kPer; ++n) off[n] = unit(n, kC - 1);
+  }
+  // the same with the offsets made on the spot, where registers are short
+  __device__ __forceinline__ void go_lean(uint32_t dst, const T* base, int L, int lane) const {
+#pragma unroll
+    for (int n = 0; n < kPer; ++n) lds_dma(base, unit(n, L - 1, lane), dst + 1024 * (n * NW + wave));
   }
   __device__ __forceinline__ void go(uint32_t dst, const T* base, int L) const {
     if (L >= kC) {
@@ -579,8 +584,6 @@ struct GdnLayout {
   T* D;          // [..][64][V]
   float* tokf;   // [..][V / 16][64]: the tokens' scalars from the forward run, per 16 columns
   float* tokr;   // [..][V / 16][64]: those from the reverse scan
-  float* dgc;    // [..][64]: sum of the scalars from a token to its chunk's end
-  double* tot;   // [..]: of the whole chunk
   float* end;    // [N * HV][V / 16]: <S_T, dS_T> of the columns
   float* par;    // [..][2]
   size_t bytes;
@@ -598,8 +601,7 @@ struct GdnLayout {
     scal = reinterpret_cast<float*>(take(n * kGdnScal * kC * sizeof(float)));
     frag = reinterpret_cast<T*>(take(n * (bwd ? GdnWs<T>::bwd : GdnWs<T>::fwd) * sizeof(T)));
     fragT = S0 = Y = dS = D = nullptr;
-    tokf = tokr = dgc = end = par = nullptr;
-    tot = nullptr;
+    tokf = tokr = end = par = nullptr;
     if (bwd) {
       fragT = reinterpret_cast<T*>(take(n * GdnWs<T>::bwd * sizeof(T)));
       S0 = reinterpret_cast<T*>(take(n * d.K * d.V * sizeof(T)));
@@ -608,8 +610,6 @@ struct GdnLayout {
       D = reinterpret_cast<T*>(take(n * kC * d.V * sizeof(T)));
       tokf = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
       tokr = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
-      dgc = reinterpret_cast<float*>(take(n * kC * sizeof(float)));
-      tot = reinterpret_cast<double*>(take(n * sizeof(double)));
       end = reinterpret_cast<float*>(take((size_t)d.N * d.HV * (d.V / 16) * sizeof(float)));
       par = reinterpret_cast<float*>(take(n * 2 * sizeof(float)));
     }

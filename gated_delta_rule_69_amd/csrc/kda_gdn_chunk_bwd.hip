@@ -5,11 +5,12 @@
 //                         state gradient, walking the chunks backwards; writes
 //                         dv, its part of the tokens' scalars, and per chunk dS
 //                         (at the chunk's end) and D.
-//   gdn_tok_kernel        the tokens' scalars of a chunk, summed to its end.
-//   gdn_local_kernel      one workgroup per (chunk, q/k head), wave w owning
-//                         token tile w: dq, dk (summed over the head's value
-//                         heads) and dbeta from the chunk's S0, Y, dS and D, and
-//                         the gate's gradient from the shares of dg.
+//   gdn_gate_bwd_kernel   bf16: the gate's gradient from the tokens' scalars,
+//                         one workgroup per chain.
+//   gdn_local_kernel      per (chunk, q/k head): dq, dk (summed over the head's
+//                         value heads) and dbeta from the chunk's S0, Y, dS and
+//                         D (gdn_local32_kernel for FP32 inputs, with the gate's
+//                         gradient).
 //   gdn_par_kernel        dA_log and d_dt_bias from per-chunk partial sums.
 //
 // With dP = dO Delta^T and dE = E Delta^T (64 x 64) the gradients of k, q are
@@ -424,33 +425,84 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
   }
 }
 
-// FP32: one wave per 16 columns, FP32 matrix cores, one operand buffer.
-// Per (chunk, value head), one wave: the tokens' scalars over all columns,
-// summed from each token to the chunk's end, and the chunk's total.
+// bf16: the gate's gradient from the tokens' scalars, one workgroup per chain:
+// 16 chunks a step from the chain's end, lane = token, wave = chunk; the sums
+// towards the end are held in double.
 template <int V>
-__global__ void __launch_bounds__(256)
-gdn_tok_kernel(const int32_t* __restrict__ cu, const int* __restrict__ table, int N, int T_, int HV, int64_t n,
-               const float* __restrict__ tokf, const float* __restrict__ tokr, float* __restrict__ dgc,
-               double* __restrict__ tot) {
-  const int lane = threadIdx.x & 63;
-  const int64_t ch = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (ch >= n) return;
-  const ChunkGeo geo = chunk_geo((int)(ch / HV), cu, table, N, T_);
-  if (!geo.ok) return;
-  double y = 0.;
-#pragma unroll
-  for (int i = 0; i < V / 16; ++i) {
-    const size_t at = ((size_t)ch * (V / 16) + i) * kC + lane;
-    y += (double)tokf[at] - (double)tokr[at];
+__global__ void __launch_bounds__(1024)
+gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __restrict__ table, int T_, int HV,
+                    int has_h0, int has_dht, const float* __restrict__ tokf, const float* __restrict__ tokr,
+                    const float* __restrict__ ends, void* __restrict__ dgate, float* __restrict__ par) {
+  constexpr int NB = V / 16;
+  __shared__ double s_tot[2][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = blockIdx.x / HV, hv = blockIdx.x % HV;
+  int64_t bos = (int64_t)n * T_;
+  int len = T_;
+  if (cu) {
+    bos = cu[n];
+    len = cu[n + 1] - cu[n];
   }
-  if (lane >= geo.L) y = 0.;
+  const int nc = (len + kC - 1) / kC;
+  if (nc <= 0) return;
+  const int64_t c0 = cu ? table[1 + n] : (int64_t)n * nc;
+  double tail = 0.;  // what lies behind the step's chunks
+  if (has_dht)
+    for (int i = 0; i < NB; ++i) tail += (double)ends[((size_t)n * HV + hv) * NB + i];
+  float x[NB], y[NB];
+  auto fetch = [&](int c) __attribute__((always_inline)) {
+    const size_t at = (size_t)((c0 + max(c, 0)) * HV + hv) * NB * kC + lane;
 #pragma unroll
-  for (int i = 1; i < 64; i <<= 1) {
-    const double z = __shfl_down(y, i);
-    if (lane + i < 64) y += z;
+    for (int i = 0; i < NB; ++i) {
+      x[i] = tokf[at + i * kC];
+      y[i] = tokr[at + i * kC];
+    }
+  };
+  fetch(nc - 1 - wave);
+  for (int top = nc, b = 0; top > 0; top -= 16, b ^= 1) {
+    const int c = top - 1 - wave;
+    const bool ok = c >= 0 && lane < min(kC, len - c * kC);
+    double s = 0.;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) s += (double)x[i] - (double)y[i];
+    if (!ok) s = 0.;
+    if (top > 16) fetch(c - 16);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const double z = __shfl_down(s, d);
+      if (lane + d < 64) s += z;
+    }
+    if (lane == 0) s_tot[b][wave] = s;
+    __syncthreads();
+    double behind = tail;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      const double z = s_tot[b][w];
+      if (w < wave) behind += z;
+      tail += z;
+    }
+    if (c < 0) continue;
+    // before a sequence's first token there is nothing to decay without a state
+    const float dg = c == 0 && lane == 0 && !has_h0 ? 0.f : (float)(s + behind);
+    float pa = 0.f, pb = 0.f;
+    if (ok) {
+      const int64_t at = (bos + (int64_t)c * kC + lane) * HV + hv;
+      float xb, as;
+      const float gn = gdn_gate(gate, at, hv, &xb, &as);
+      const float dx = gate.raw ? -dg * as * sigmoid_f32(xb) : dg;
+      st_any(dgate, at, gate.bf, dx);
+      pa = dg * gn;  // dg / dA_log = g
+      pb = dx;
+    }
+    if (gate.A_log || gate.dt_bias) {
+#pragma unroll
+      for (int d = 32; d; d >>= 1) {
+        pa += __shfl_xor(pa, d);
+        pb += __shfl_xor(pb, d);
+      }
+      if (lane == 0) *reinterpret_cast<float2*>(par + 2 * ((c0 + c) * HV + hv)) = make_float2(pa, pb);
+    }
   }
-  dgc[ch * kC + lane] = (float)y;
-  if (lane == 0) tot[ch] = y;
 }
 
 // FP32: one wave per 16 columns, FP32 matrix cores, one operand buffer.
@@ -612,23 +664,352 @@ __device__ __forceinline__ float op_dot(const Op8<T>& a, const Op8<T>& b) {
   return s;
 }
 
-template <typename T, int K, int V>
-__global__ void __launch_bounds__(256)
-gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ dO, GdnGate gate,
-                 const int32_t* __restrict__ cu, const int* __restrict__ table, int N, int T_, int H,
-                 int HV, int l2, int has_h0, float scale, const float* __restrict__ ws_scal,
-                 const T* __restrict__ ws_S0, const T* __restrict__ ws_Y, const T* __restrict__ ws_dS,
-                 const T* __restrict__ ws_D, const float* __restrict__ ws_dgc, const double* __restrict__ ws_tot,
-                 const float* __restrict__ ws_end, int has_dht, T* __restrict__ dq, T* __restrict__ dk,
-                 T* __restrict__ dbeta, void* __restrict__ dgate, float* __restrict__ par) {
+// bf16. Eight waves: wave w and wave w + 4 own token tile w. The first four
+// form what takes a token as the later of a pair (from S0, Y: dq and a part of
+// dk), the others what takes it as the earlier (from dS, dO, D: dbeta and the
+// rest of dk). The kernel moves 180 KB for some 2 us of products, so one
+// workgroup stays on a CU, walks its (chunk, head) items and keeps two sets of
+// transfers into LDS going: S0, dS, k and q arrive while the 64 x 64 products
+// run over Y, D and dO, and the next item's Y, D and dO while the channel tiles
+// run over S0 and dS.
+template <int K, int V>
+struct GdnLocalLds {
+  static constexpr uint32_t tok = TokTile<bf16, K>::bytes, st = K * V * sizeof(bf16), row = kC * V * sizeof(bf16);
+  static constexpr uint32_t scal = kGdnScal * kC * sizeof(float);
+  static constexpr uint32_t oQ = tok, oS = oQ + tok, odS = oS + st, oY = odS + st, oD = oY + row, oO = oD + row;
+  static constexpr uint32_t oF = oO + row, total = oF + 2 * scal;
+  static_assert(2 * st >= (K / 16) * 4 * 1024, "dk's exchange fits S0 and dS");
+};
+
+template <int K, int V>
+__global__ void __launch_bounds__(512, 2)
+gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ dO,
+                 const int32_t* __restrict__ cu, const int* __restrict__ table, int chunks, int N, int T_, int H,
+                 int HV, int l2, float scale, const float* __restrict__ ws_scal, const bf16* __restrict__ ws_S0,
+                 const bf16* __restrict__ ws_Y, const bf16* __restrict__ ws_dS, const bf16* __restrict__ ws_D,
+                 bf16* __restrict__ dq, bf16* __restrict__ dk, bf16* __restrict__ dbeta) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
+  using L_ = GdnLocalLds<K, V>;
+  using TT = TokTile<bf16, K>;
+  using TV = TokTile<bf16, V>;
+  constexpr int NV = V / 32, RT = K / 16;
+  const int w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = w8 & 3;
+  const bool later = w8 < 4;
+  const int grp = HV / H;
+  const char *sK = smem, *sQ = smem + L_::oQ;
+  const bf16* sS0 = reinterpret_cast<const bf16*>(smem + L_::oS);
+  const bf16* sdS = reinterpret_cast<const bf16*>(smem + L_::odS);
+  const bf16* sY = reinterpret_cast<const bf16*>(smem + L_::oY);
+  const bf16* sD = reinterpret_cast<const bf16*>(smem + L_::oD);
+  const char* sO = smem + L_::oO;
+  char* sx = smem + L_::oS;  // exchange of dk, once S0 and dS are read
+  const uint32_t lds = lds_addr(smem);
+  const TokDma<bf16, K, 8> tok((uint32_t)(H * K * sizeof(bf16)), w8);
+  const TokDma<bf16, V, 8> tov((uint32_t)(HV * V * sizeof(bf16)), w8);
+  const int p = wave >> 1;  // 32-token block of the wave's tokens
+
+  // the transfers a wave issues for Y, D and dO of one value head, row factors first
+  constexpr int kRowDma = 2 * (int)(L_::row / 8192) + TokDma<bf16, V, 8>::kPer;
+  auto fetch_rows = [&](int64_t t0, int L, int64_t ch, int hv, int buf, int lane) __attribute__((always_inline)) {
+    dma_flat<L_::scal, 8>(lds + L_::oF + buf * L_::scal, ws_scal + ch * (kGdnScal * kC), w8);
+    dma_flat<L_::row, 8>(lds + L_::oY, ws_Y + ch * kC * V, w8);
+    dma_flat<L_::row, 8>(lds + L_::oD, ws_D + ch * kC * V, w8);
+    tov.go_lean(lds + L_::oO, dO + (t0 * HV + hv) * V, L, lane);
+  };
+  auto fetch_states = [&](int64_t ch) __attribute__((always_inline)) {
+    dma_flat<L_::st, 8>(lds + L_::oS, ws_S0 + ch * K * V, w8);
+    dma_flat<L_::st, 8>(lds + L_::odS, ws_dS + ch * K * V, w8);
+  };
+
+  const int items = (cu ? table[0] : chunks) * H;
+  int it = blockIdx.x;
+  if (it >= items) return;
+  ChunkGeo geo = chunk_geo(it / H, cu, table, N, T_);
+  fetch_rows(geo.t0, geo.L, (int64_t)(it / H) * HV + (it % H) * grp, (it % H) * grp, 0, threadIdx.x & 63);
+  lds_dma_wait();
+  int buf = 0;
+  for (; it < items; it += gridDim.x) {
+    const int j = it / H, h = it % H, L = geo.L;
+    const int64_t t0 = geo.t0;
+    f32x4 aq[RT], ak[RT];  // aq: the first four waves only
+#pragma unroll
+    for (int r = 0; r < RT; ++r) aq[r] = ak[r] = zero4();
+    const int nxt = it + gridDim.x;
+    if (nxt < items) geo = chunk_geo(nxt / H, cu, table, N, T_);
+
+    for (int hh = 0; hh < grp; ++hh, buf ^= 1) {
+      const int hv = h * grp + hh;
+      const int64_t ch = (int64_t)j * HV + hv;
+      const float* sc = reinterpret_cast<const float*>(smem + L_::oF + buf * L_::scal);
+      const double* sG = reinterpret_cast<const double*>(sc + kSG * kC);
+      // the lane is made anew for each round: kept over all of them, the LDS addresses made from
+      // it filled the registers, and what spills waits for the transfers under way
+      int lane = threadIdx.x & 63;
+      asm volatile("" : "+v"(lane));
+      const int g = lane >> 4, l16 = lane & 15;
+      const int own = perm_row(wave, l16);  // this lane's row as an operand
+      const int own4 = perm_row4(wave, g);  // first of its four accumulator rows
+      __syncthreads();  // Y, D, dO and the row factors are in LDS; S0, dS, k and q are read
+      if (hh == 0) {
+        tok.go_lean(lds, k + (t0 * H + h) * K, L, lane);
+        tok.go_lean(lds + L_::oQ, q + (t0 * H + h) * K, L, lane);
+      }
+      fetch_states(ch);
+
+      // 64 x 64 parts. As rows (contraction over j): W_ij = e_ij b_j rk_j / sqrt(K) dO_i.Y_j and
+      // Z_ij = - e_ij b_i b_j rk_j D_i.Y_j, from the products with Y's rows on the left, so the
+      // accumulators are the operand with the wave's tokens as rows. As columns (contraction
+      // over i): W'_ij = e_ij b_j rq_i / sqrt(K) dO_i.Y_j, Z'_ij = - e_ij b_i b_j rk_i D_i.Y_j.
+      Op8<bf16> oa[NV], ob[NV];  // own rows: dO and D; Y
+      Op8<bf16> wo[2], zo[2];
+      const double Go = sG[own];
+      const float bo = sc[kSb * kC + own];
+      if (later) {
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          TV::rows(oa[u], sO, wave, u, lane);
+          op_ld(ob[u], sD, wave, u, NV, lane);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          f32x4 w[2], z[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) w[i] = z[i] = zero4();
+          if (s <= p) {
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                Op8<bf16> y;
+                op_ld(y, sY, 2 * s + i, u, NV, lane);
+                w[i] = mma8(y, oa[u], w[i]);
+                z[i] = mma8(y, ob[u], z[i]);
+              }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row4 = perm_row4(2 * s + i, g);
+              float b4[4], rk_[4];
+              float gg[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                gg[e] = (float)(Go - sG[row4 + e]);
+                settle(gg[e]);  // no branch around the read
+              }
+              lds4(sc + kSb * kC + row4, b4);
+              lds4(sc + kSrk * kC + row4, rk_);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int o = row4 + e;  // the earlier token
+                const float ej = ex2((own >= o) & (own < L) ? gg[e] : -INFINITY) * b4[e] * rk_[e];
+                w[i][e] *= ej * scale;
+                z[i][e] *= own > o ? -ej * bo : 0.f;
+              }
+            }
+          }
+          make_op(wo[s], w[0], w[1]);
+          make_op(zo[s], z[0], z[1]);
+          stage();
+        }
+      } else {
+        float x = 0.f;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+          op_ld(oa[u], sY, wave, u, NV, lane);
+          Op8<bf16> d;
+          op_ld(d, sD, wave, u, NV, lane);
+          x += op_dot(d, oa[u]);
+        }
+        x += __shfl_xor(x, 16);
+        x += __shfl_xor(x, 32);
+        if (g == 0 && own < L) dbeta[(t0 + own) * HV + hv] = from_f32<bf16>(x);  // <D_i, Y_i>
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          f32x4 w[2], z[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) w[i] = z[i] = zero4();
+          if (s >= p) {
+#pragma unroll
+            for (int u = 0; u < NV; ++u)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                Op8<bf16> a, d;
+                TV::rows(a, sO, 2 * s + i, u, lane);
+                op_ld(d, sD, 2 * s + i, u, NV, lane);
+                w[i] = mma8(a, oa[u], w[i]);
+                z[i] = mma8(d, oa[u], z[i]);
+              }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row4 = perm_row4(2 * s + i, g);
+              float b4[4], rq_[4], rk_[4];
+              float gg[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                gg[e] = (float)(Go - sG[row4 + e]);
+                settle(gg[e]);  // no branch around the read
+              }
+              lds4(sc + kSb * kC + row4, b4);
+              lds4(sc + kSrq * kC + row4, rq_);
+              lds4(sc + kSrk * kC + row4, rk_);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int o = row4 + e;  // the later token
+                const float ei = ex2((o >= own) & (o < L) ? -gg[e] : -INFINITY) * bo;
+                w[i][e] *= ei * rq_[e] * scale;
+                z[i][e] *= o > own ? -ei * b4[e] * rk_[e] : 0.f;
+              }
+            }
+          }
+          make_op(wo[s], w[0], w[1]);
+          make_op(zo[s], z[0], z[1]);
+          stage();
+        }
+      }
+      // the next value head's rows, or the next item's
+      const bool more = hh + 1 < grp;
+      __syncthreads();  // Y, D and dO are read
+      if (more || nxt < items) {
+        const int nj = more ? j : nxt / H, nhv = more ? hv + 1 : (nxt % H) * grp;
+        fetch_rows(more ? t0 : geo.t0, more ? L : geo.L, (int64_t)nj * HV + nhv, nhv, buf ^ 1, lane);
+        lds_dma_wait_but<kRowDma>();
+      } else {
+        lds_dma_wait();
+      }
+      __syncthreads();  // S0, dS, k and q are in LDS
+
+      // channel tiles (a block of pairs that none of the tile's tokens has is zero in wo and zo; a
+      // branch around it costs more). fq = e^G rq / sqrt(K), fk = e^G rk, fe = e^{G_last - G} rk: gradients of
+      // the normalised rows, times their own inverse norm
+      float fb[4], frk[4];
+      lds4(sc + kSb * kC + own4, fb);
+      lds4(sc + kSrk * kC + own4, frk);
+      if (later) {
+        float fk[4], fq[4], frq[4];
+        lds4(sc + kSk * kC + own4, fk);
+        lds4(sc + kSq * kC + own4, fq);
+        lds4(sc + kSrq * kC + own4, frq);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) fk[e] *= -fb[e];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          f32x4 a1 = zero4(), a2 = zero4(), tq = zero4(), tr = zero4();
+#pragma unroll
+          for (int s = 0; s < NV; ++s) {
+            Op8<bf16> x;
+            op_ld(x, sS0, r, s, NV, lane);
+            a1 = mma8(oa[s], x, a1);
+            a2 = mma8(ob[s], x, a2);
+          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            Op8<bf16> kc;
+            TT::cols(kc, sK, r, s, lane);
+            tq = mma8(wo[s], kc, tq);
+            tr = mma8(zo[s], kc, tr);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            aq[r][e] += a1[e] * fq[e] + frq[e] * tq[e];
+            ak[r][e] += a2[e] * fk[e] + frk[e] * tr[e];
+          }
+          stage();  // one tile's operands live at a time
+        }
+      } else {
+        float fe[4];
+        lds4(sc + kSe * kC + own4, fe);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) fe[e] *= fb[e];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          f32x4 a3 = zero4(), tc = zero4();
+#pragma unroll
+          for (int s = 0; s < NV; ++s) {
+            Op8<bf16> x;
+            op_ld(x, sdS, r, s, NV, lane);
+            a3 = mma8(oa[s], x, a3);
+          }
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            Op8<bf16> kc, qc;
+            TT::cols(kc, sK, r, s, lane);
+            TT::cols(qc, sQ, r, s, lane);
+            tc = mma8(wo[s], qc, tc);
+            tc = mma8(zo[s], kc, tc);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ak[r][e] += a3[e] * fe[e] + frk[e] * tc[e];
+          stage();
+        }
+      }
+      if (more) lds_dma_wait();
+      if (!more) {
+        // dk's first part to the wave with the other; then each finishes one gradient
+        float rn[4];
+        lds4(sc + (later ? kSrq : kSrk) * kC + own4, rn);
+        lds_dma_wait();   // before the stores below, not behind them
+        __syncthreads();  // S0 and dS are read
+        f32x4* x = reinterpret_cast<f32x4*>(sx) + (wave * RT) * 64 + lane;
+        if (later) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) x[r * 64] = ak[r];
+        }
+        __syncthreads();
+        if (!later) {
+          f32x4 y[RT];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) y[r] = x[r * 64];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) aq[r] = ak[r] + y[r];
+        }
+        const char* sT = later ? sQ : sK;
+        // through the L2 norm: q^ = rq q, so dq = rq (dq^ - q^ <q^, dq^>); aq holds rq dq^
+        if (l2) {
+          float nn[4] = {0.f, 0.f, 0.f, 0.f};
+          f32x4 xt[RT];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            xt[r] = TT::tile(sT, wave, r, lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) nn[e] = fmaf(xt[r][e], aq[r][e], nn[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) nn[e] = row16_sum(nn[e]) * rn[e] * rn[e];
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) aq[r][e] = fmaf(-xt[r][e], nn[e], aq[r][e]);
+        }
+        const int row = own4 + (l16 & 3);
+        bf16* out = (later ? dq : dk) + ((t0 + row) * H + h) * K + 8 * (l16 >> 2);
+        uint2 y[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) y[r] = quad_transpose(pack4(aq[r]));
+        if (row < L) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r) *reinterpret_cast<uint2*>(out + 32 * (r >> 1) + 4 * (r & 1)) = y[r];
+        }
+      }
+    }
+  }
+}
+
+// FP32. Four waves, one per token tile, operands straight from memory.
+template <int K, int V>
+__global__ void __launch_bounds__(256)
+gdn_local32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dO, GdnGate gate,
+                   const int32_t* __restrict__ cu, const int* __restrict__ table, int N, int T_, int H,
+                   int HV, int l2, int has_h0, float scale, const float* __restrict__ ws_scal,
+                   const float* __restrict__ ws_S0, const float* __restrict__ ws_Y, const float* __restrict__ ws_dS,
+                   const float* __restrict__ ws_D, float* __restrict__ dq, float* __restrict__ dk,
+                   float* __restrict__ dbeta, void* __restrict__ dgate, float* __restrict__ par) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  using T = float;
   using TT = TokTile<T, K>;
   constexpr int NV = V / 32, RT = K / 16;
   __shared__ double sG[kC];
-  constexpr bool kDirect = !GdnWs<T>::kScanGate;
   __shared__ __attribute__((aligned(16))) float sB[kC];
-  __shared__ __attribute__((aligned(16))) float sR[kDirect ? kC : 4], sC[kDirect ? kC : 4];
-  __shared__ float sS[4], sX[kDirect ? kC : 1], sXc[4][kDirect ? kC : 1];
+  __shared__ __attribute__((aligned(16))) float sR[kC], sC[kC];
+  __shared__ float sS[4], sX[kC], sXc[4][kC];
   const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int j = blockIdx.x / H, h = blockIdx.x % H, grp = HV / H;
@@ -707,17 +1088,15 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
       for (int i = 0; i < 2; ++i) {
         const int row = perm_row(2 * s + i, l16), row4 = perm_row4(2 * s + i, g);
         f32x4 qk = zero4(), kk = zero4();
-        if constexpr (kDirect) {
-          if (s <= p) {
+        if (s <= p) {
 #pragma unroll
-            for (int u = 0; u < K / 32; ++u) {
-              Op8<T> kj, qi, ki;
-              TT::rows(kj, sK, 2 * s + i, u);
-              TT::rows(qi, sQ, wave, u);
-              TT::rows(ki, sK, wave, u);
-              qk = mma8(kj, qi, qk);
-              kk = mma8(kj, ki, kk);
-            }
+          for (int u = 0; u < K / 32; ++u) {
+            Op8<T> kj, qi, ki;
+            TT::rows(kj, sK, 2 * s + i, u);
+            TT::rows(qi, sQ, wave, u);
+            TT::rows(ki, sK, wave, u);
+            qk = mma8(kj, qi, qk);
+            kk = mma8(kj, ki, kk);
           }
         }
         if (s <= p) {
@@ -753,12 +1132,10 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
           z[i][e] = own > o ? -z[i][e] * ej * bo : 0.f;
           w2[i][e] *= ei * rq_[e] * scale;
           z2[i][e] = o > own ? -z2[i][e] * ei * b4[e] * rk_[e] : 0.f;
-          if constexpr (kDirect) {
-            const float x = own > o ? w[i][e] * rqo * qk[e] + z[i][e] * rko * kk[e] : 0.f;
-            xrow += x;
-            const float xc = row16_sum(x);
-            if (l16 == 0) sXc[wave][o] = xc;
-          }
+          const float x = own > o ? w[i][e] * rqo * qk[e] + z[i][e] * rko * kk[e] : 0.f;
+          xrow += x;
+          const float xc = row16_sum(x);
+          if (l16 == 0) sXc[wave][o] = xc;
         }
       }
       make_op(wr[s], w[0], w[1]);
@@ -766,11 +1143,9 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
       make_op(wc[s], w2[0], w2[1]);
       make_op(zc[s], z2[0], z2[1]);
     }
-    if constexpr (kDirect) {
-      xrow += __shfl_xor(xrow, 16);
-      xrow += __shfl_xor(xrow, 32);
-      if (g == 0) sX[own] = xrow;
-    }
+    xrow += __shfl_xor(xrow, 16);
+    xrow += __shfl_xor(xrow, 32);
+    if (g == 0) sX[own] = xrow;
     // channel tiles
     float rr[4] = {0.f, 0.f, 0.f, 0.f}, cc[4] = {0.f, 0.f, 0.f, 0.f}, sds = 0.f;
     const T* S0b = ws_S0 + ch * K * V;
@@ -786,9 +1161,7 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
         a1 = mma8(od[s], s0, a1);
         a2 = mma8(oD[s], s0, a2);
         a3 = mma8(oY[s], ds, a3);
-        if constexpr (kDirect) {
-          if ((r & 3) == wave) sds += op_dot(s0, ds);
-        }
+        if ((r & 3) == wave) sds += op_dot(s0, ds);
       }
       f32x4 tq = zero4(), tr = zero4(), tc = zero4();
 #pragma unroll
@@ -812,59 +1185,44 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
         aq[r][e] += a1[e] * fq[e] + frq[e] * tq[e];
         ak[r][e] += (a3[e] * fe[e] - a2[e] * fk[e]) * fb[e] + frk[e] * (tr[e] + tc[e]);
       }
-      if constexpr (kDirect) {
-        const f32x4 qt = TT::tile(sQ, wave, r), kt = TT::tile(sK, wave, r);
+      const f32x4 qt = TT::tile(sQ, wave, r), kt = TT::tile(sK, wave, r);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          rr[e] += qt[e] * a1[e] * fq[e] - kt[e] * a2[e] * fk[e] * fb[e];
-          cc[e] += kt[e] * a3[e] * fe[e] * fb[e];
-        }
+      for (int e = 0; e < 4; ++e) {
+        rr[e] += qt[e] * a1[e] * fq[e] - kt[e] * a2[e] * fk[e] * fb[e];
+        cc[e] += kt[e] * a3[e] * fe[e] * fb[e];
       }
       __builtin_amdgcn_sched_barrier(0);  // one tile's operands live at a time
     }
-    if constexpr (kDirect) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        rr[e] = row16_sum(rr[e]);
-        cc[e] = row16_sum(cc[e]);
-      }
-      sds = row16_sum(sds);
-      sds += __shfl_xor(sds, 16);
-      sds += __shfl_xor(sds, 32);
-      if (l16 == 0) {
-        *reinterpret_cast<float4*>(sR + own4) = make_float4(rr[0], rr[1], rr[2], rr[3]);
-        *reinterpret_cast<float4*>(sC + own4) = make_float4(cc[0], cc[1], cc[2], cc[3]);
-      }
-      if (lane == 0) sS[wave] = sds;
-      __syncthreads();
+    for (int e = 0; e < 4; ++e) {
+      rr[e] = row16_sum(rr[e]);
+      cc[e] = row16_sum(cc[e]);
     }
+    sds = row16_sum(sds);
+    sds += __shfl_xor(sds, 16);
+    sds += __shfl_xor(sds, 32);
+    if (l16 == 0) {
+      *reinterpret_cast<float4*>(sR + own4) = make_float4(rr[0], rr[1], rr[2], rr[3]);
+      *reinterpret_cast<float4*>(sC + own4) = make_float4(cc[0], cc[1], cc[2], cc[3]);
+    }
+    if (lane == 0) sS[wave] = sds;
+    __syncthreads();
     if (wave == 0) {
       const bool ok = lane < L;
       float dg = 0.f;
-      if constexpr (kDirect) {
-        float r = 0.f, c = 0.f;
-        if (ok) {
-          r = sR[lane] + (sX[lane] - ((sXc[0][lane] + sXc[1][lane]) + (sXc[2][lane] + sXc[3][lane])));
-          c = sC[lane];
-        }
-        const float c_own = c;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const float x = __shfl_down(r, d), y = __shfl_up(c, d);
-          if (lane + d < 64) r += x;
-          if (lane >= d) c += y;
-        }
-        dg = r + (c - c_own) + sc[kSl * kC] * ((sS[0] + sS[1]) + (sS[2] + sS[3]));
-      } else {
-        // tokens from this one to its chunk's end, the chunks behind, and the end itself
-        double y = 0.;
-        const int last = cu ? table[2 + geo.n] : (geo.n + 1) * ((T_ + kC - 1) / kC);  // end of the sequence's chunks
-        for (int c2 = j + 1 + lane; c2 < last; c2 += 64) y += ws_tot[(size_t)c2 * HV + hv];
-        if (has_dht && lane < V / 16) y += (double)ws_end[((size_t)geo.n * HV + hv) * (V / 16) + lane];
-#pragma unroll
-        for (int d = 32; d; d >>= 1) y += __shfl_xor(y, d);
-        dg = (float)((double)ws_dgc[ch * kC + lane] + y);
+      float r = 0.f, c = 0.f;
+      if (ok) {
+        r = sR[lane] + (sX[lane] - ((sXc[0][lane] + sXc[1][lane]) + (sXc[2][lane] + sXc[3][lane])));
+        c = sC[lane];
       }
+      const float c_own = c;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const float x = __shfl_down(r, d), y = __shfl_up(c, d);
+        if (lane + d < 64) r += x;
+        if (lane >= d) c += y;
+      }
+      dg = r + (c - c_own) + sc[kSl * kC] * ((sS[0] + sS[1]) + (sS[2] + sS[3]));
       // before a sequence's first token there is nothing to decay without a state
       if (geo.c == 0 && lane == 0 && !has_h0) dg = 0.f;
       float pa = 0.f, pb = 0.f;
@@ -926,22 +1284,13 @@ gdn_local_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __re
   const int64_t out = (geo.t0 * H + h) * K;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    if constexpr (sizeof(T) == 2) {
-      const int row = own4 + (l16 & 3), col = 32 * (r >> 1) + 8 * (l16 >> 2) + 4 * (r & 1);
-      const uint2 x = quad_transpose(pack4(aq[r])), y = quad_transpose(pack4(ak[r]));
-      if (row < L) {
-        *reinterpret_cast<uint2*>(dq + out + (int64_t)row * H * K + col) = x;
-        *reinterpret_cast<uint2*>(dk + out + (int64_t)row * H * K + col) = y;
-      }
-    } else {
-      const int col = perm_row(r, l16);
+    const int col = perm_row(r, l16);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (own4 + e < L) {
-          dq[out + (int64_t)(own4 + e) * H * K + col] = aq[r][e];
-          dk[out + (int64_t)(own4 + e) * H * K + col] = ak[r][e];
-        }
-    }
+    for (int e = 0; e < 4; ++e)
+      if (own4 + e < L) {
+        dq[out + (int64_t)(own4 + e) * H * K + col] = aq[r][e];
+        dk[out + (int64_t)(own4 + e) * H * K + col] = ak[r][e];
+      }
   }
 }
 
@@ -1002,6 +1351,41 @@ static hipError_t rev_t(const kda_dims& d, const void* q, const void* k, const v
   return hipGetLastError();
 }
 
+template <int K, int V>
+static hipError_t local_t(const kda_dims& d, const void* q, const void* k, const void* dO, const GdnGate& gate, int l2,
+                          int has_h0, int has_dht, const int32_t* cu, const GdnLayout<bf16>& w, void* dq, void* dk,
+                          void* dbeta, void* dgate, hipStream_t s) {
+  hipLaunchKernelGGL((gdn_gate_bwd_kernel<V>), dim3((unsigned)(d.N * d.HV)), dim3(1024), 0, s, gate, cu, w.table, d.T,
+                     d.HV, has_h0, has_dht, w.tokf, w.tokr, w.end, dgate, w.par);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  constexpr size_t lds = GdnLocalLds<K, V>::total;
+  static_assert(lds <= 160 * 1024, "LDS");
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_local_kernel<K, V>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  const int64_t mc = max_chunks(d, cu != nullptr);
+  const int64_t wgs = std::min<int64_t>(mc * d.H, kda_host::device_cus());
+  hipLaunchKernelGGL((gdn_local_kernel<K, V>), dim3((unsigned)wgs), dim3(512), lds, s, (const bf16*)q, (const bf16*)k,
+                     (const bf16*)dO, cu, w.table, (int)mc, d.N, d.T, d.H, d.HV, l2, 1.0f / sqrtf((float)K), w.scal,
+                     w.S0, w.Y, w.dS, w.D, (bf16*)dq, (bf16*)dk, (bf16*)dbeta);
+  return hipGetLastError();
+}
+template <int K, int V>
+static hipError_t local_t(const kda_dims& d, const void* q, const void* k, const void* dO, const GdnGate& gate, int l2,
+                          int has_h0, int, const int32_t* cu, const GdnLayout<float>& w, void* dq, void* dk,
+                          void* dbeta, void* dgate, hipStream_t s) {
+  constexpr size_t lds = 2 * TokTile<float, K>::bytes;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_local32_kernel<K, V>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((gdn_local32_kernel<K, V>), dim3((unsigned)(max_chunks(d, cu != nullptr) * d.H)), dim3(256), lds,
+                     s, (const float*)q, (const float*)k, (const float*)dO, gate, cu, w.table, d.N, d.T, d.H, d.HV, l2,
+                     has_h0, 1.0f / sqrtf((float)K), w.scal, w.S0, w.Y, w.dS, w.D, (float*)dq, (float*)dk,
+                     (float*)dbeta, dgate, w.par);
+  return hipGetLastError();
+}
+
 template <typename T, int K, int V>
 static hipError_t gdn_bwd_kv(const kda_dims& d, const void* q, const void* k, const void* v, const GdnGate& gate, int l2,
                              const float* h0, const int32_t* cu, const void* dO, const float* dht, void* dq,
@@ -1013,22 +1397,7 @@ static hipError_t gdn_bwd_kv(const kda_dims& d, const void* q, const void* k, co
   if (d.N > 0) e = rev_t<K, V, 2>(d, q, k, v, dO, dht, cu, w, dv, dh0, s);
   if (e != hipSuccess) return e;
   if (d.N > 0 && mc > 0) {
-    if constexpr (GdnWs<T>::kScanGate) {
-      const int64_t n = mc * d.HV;
-      hipLaunchKernelGGL((gdn_tok_kernel<V>), dim3((unsigned)((n + 3) / 4)), dim3(256), 0, s, cu, w.table, d.N, d.T,
-                         d.HV, n, w.tokf, w.tokr, w.dgc, w.tot);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-    constexpr size_t lds = 2 * TokTile<T, K>::bytes;
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_local_kernel<T, K, V>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((gdn_local_kernel<T, K, V>), dim3((unsigned)(mc * d.H)), dim3(256), lds, s,
-                       (const T*)q, (const T*)k, (const T*)dO, gate, cu, w.table, d.N, d.T, d.H, d.HV, l2,
-                       h0 != nullptr ? 1 : 0, 1.0f / sqrtf((float)K), w.scal, w.S0, w.Y, w.dS, w.D, w.dgc, w.tot, w.end,
-                       dht != nullptr ? 1 : 0, (T*)dq, (T*)dk, (T*)dbeta, dgate, w.par);
-    e = hipGetLastError();
+    e = local_t<K, V>(d, q, k, dO, gate, l2, h0 != nullptr, dht != nullptr, cu, w, dq, dk, dbeta, dgate, s);
     if (e != hipSuccess) return e;
   }
   if (dA || ddt) {
