@@ -449,7 +449,9 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
   double tail = 0.;  // what lies behind the step's chunks
   if (has_dht)
     for (int i = 0; i < NB; ++i) tail += (double)ends[((size_t)n * HV + hv) * NB + i];
-  float x[NB], y[NB];
+  const float as = gate.raw && gate.A_log ? expf(ld_any(gate.A_log, hv, gate.bf)) : 1.f;
+  const float bias = gate.raw && gate.dt_bias ? ld_any(gate.dt_bias, hv, gate.bf) : 0.f;
+  float x[NB], y[NB], gx = 0.f;
   auto fetch = [&](int c) __attribute__((always_inline)) {
     const size_t at = (size_t)((c0 + max(c, 0)) * HV + hv) * NB * kC + lane;
 #pragma unroll
@@ -457,6 +459,8 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
       x[i] = tokf[at + i * kC];
       y[i] = tokr[at + i * kC];
     }
+    const int t = min(max(c, 0) * kC + lane, len - 1);
+    gx = ld_any(gate.x, (bos + t) * HV + hv, gate.bf);
   };
   fetch(nc - 1 - wave);
   for (int top = nc, b = 0; top > 0; top -= 16, b ^= 1) {
@@ -466,6 +470,7 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
 #pragma unroll
     for (int i = 0; i < NB; ++i) s += (double)x[i] - (double)y[i];
     if (!ok) s = 0.;
+    const float xb = gate.dt_bias ? gx + bias : gx;
     if (top > 16) fetch(c - 16);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -487,8 +492,7 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
     float pa = 0.f, pb = 0.f;
     if (ok) {
       const int64_t at = (bos + (int64_t)c * kC + lane) * HV + hv;
-      float xb, as;
-      const float gn = gdn_gate(gate, at, hv, &xb, &as);
+      const float gn = gate.raw ? -as * softplus_f32(xb) : xb;
       const float dx = gate.raw ? -dg * as * sigmoid_f32(xb) : dg;
       st_any(dgate, at, gate.bf, dx);
       pa = dg * gn;  // dg / dA_log = g

@@ -30,16 +30,18 @@ struct NormArgs {
   float eps;
 };
 
+// VEC elements as they lie in memory
 template <typename T, int VEC>
-__device__ __forceinline__ void vec_ld(float* x, const T* p) {
+using VecRaw = std::conditional_t<VEC == 1, T, uint4>;
+template <typename T, int VEC>
+__device__ __forceinline__ void vec_get(float* x, const VecRaw<T, VEC>& p) {
   if constexpr (VEC == 1) {
-    x[0] = to_f32(p[0]);
+    x[0] = to_f32(p);
   } else if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p);
+    const float4 a = __builtin_bit_cast(float4, p);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const f32x4 lo = unpack4(make_uint2(a.x, a.y)), hi = unpack4(make_uint2(a.z, a.w));
+    const f32x4 lo = unpack4(make_uint2(p.x, p.y)), hi = unpack4(make_uint2(p.z, p.w));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       x[e] = lo[e];
@@ -113,24 +115,34 @@ norm_kernel(NormArgs a) {
       b[u * VEC + e] = a.b && c < D ? ld_any(a.b, c, a.wbf) : 0.f;
       if constexpr (BWD) dw[u * VEC + e] = db[u * VEC + e] = 0.f;
     }
+  using R = VecRaw<T, VEC>;
   // whole workgroups step together (the G = 256 sums hold a barrier)
   for (int64_t r0 = (int64_t)blockIdx.x * GPW; r0 < rows; r0 += (int64_t)gridDim.x * GPW) {
     const int64_t row = r0 + grp;
     const bool live = row < rows;
-    const int64_t off = (live ? row : 0) * D;
+    // rows and columns past the end repeat the last ones: no branch around a load
+    const int64_t off = min(row, rows - 1) * D;
+    R rx[NU], rz[NU], ry[BWD ? NU : 1];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int64_t at = off + min((u * G + gl) * VEC, D - VEC);
+      rx[u] = *reinterpret_cast<const R*>(reinterpret_cast<const T*>(a.x) + at);
+      if (a.z) rz[u] = *reinterpret_cast<const R*>(reinterpret_cast<const T*>(a.z) + at);
+      if constexpr (BWD) ry[u] = *reinterpret_cast<const R*>(reinterpret_cast<const T*>(a.dy) + at);
+    }
     float x[E], z[E], dy[BWD ? E : 1];
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const int c = (u * G + gl) * VEC;
+      const bool in = (u * G + gl) * VEC < D && live;
+      vec_get<T, VEC>(x + u * VEC, rx[u]);
+      if (a.z) vec_get<T, VEC>(z + u * VEC, rz[u]);
+      if constexpr (BWD) vec_get<T, VEC>(dy + u * VEC, ry[u]);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        x[u * VEC + e] = z[u * VEC + e] = 0.f;
-        if constexpr (BWD) dy[u * VEC + e] = 0.f;
-      }
-      if (c < D && live) {
-        vec_ld<T, VEC>(x + u * VEC, reinterpret_cast<const T*>(a.x) + off + c);
-        if (a.z) vec_ld<T, VEC>(z + u * VEC, reinterpret_cast<const T*>(a.z) + off + c);
-        if constexpr (BWD) vec_ld<T, VEC>(dy + u * VEC, reinterpret_cast<const T*>(a.dy) + off + c);
+        const int i = u * VEC + e;
+        x[i] = in ? x[i] : 0.f;
+        z[i] = in && a.z ? z[i] : 0.f;
+        if constexpr (BWD) dy[i] = in ? dy[i] : 0.f;
       }
     }
     if (a.layer) {
@@ -248,23 +260,39 @@ norm_kernel(NormArgs a) {
   }
 }
 
-// dweight, dbias: the workgroups' partial rows added in a fixed order (16 rows
-// apart per thread, then the 16 sums in order, in double)
-__global__ void __launch_bounds__(256)
+// dweight, dbias: the workgroups' partial rows added in a fixed order (32 rows
+// apart per thread, then the 32 sums in order, in double)
+__global__ void __launch_bounds__(512)
 norm_reduce_kernel(const float* __restrict__ part, int wgs, int D, int wbf, void* dw, void* db) {
-  __shared__ double s[2][16][17];
+  __shared__ double s[2][32][17];
   const int cl = threadIdx.x & 15, rl = threadIdx.x >> 4, c = blockIdx.x * 16 + cl;
   double a = 0., b = 0.;
-  if (c < D)
-    for (int i = rl; i < wgs; i += 16) {
-      a += part[(size_t)i * 2 * D + c];
-      if (db) b += part[(size_t)i * 2 * D + D + c];
+  if (c < D) {
+    const float* p = part + c;
+    int i = rl;
+    for (; i + 96 < wgs; i += 128) {
+      float x[4], y[4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        x[n] = p[(size_t)(i + 32 * n) * 2 * D];
+        y[n] = p[(size_t)(i + 32 * n) * 2 * D + D];
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        a += x[n];
+        b += y[n];
+      }
     }
+    for (; i < wgs; i += 32) {
+      a += p[(size_t)i * 2 * D];
+      b += p[(size_t)i * 2 * D + D];
+    }
+  }
   s[0][rl][cl] = a;
   s[1][rl][cl] = b;
   __syncthreads();
   if (rl == 0 && c < D) {
-    for (int i = 1; i < 16; ++i) {
+    for (int i = 1; i < 32; ++i) {
       a += s[0][i][cl];
       b += s[1][i][cl];
     }
@@ -274,10 +302,15 @@ norm_reduce_kernel(const float* __restrict__ part, int wgs, int D, int wbf, void
 }
 
 // Workgroups of a launch: each group of lanes gets a row, up to 8 (forward) or
-// 4 (backward, which also writes a partial row per workgroup) workgroups per
-// compute unit, after which the groups stride over the rows.
+// kNormBwdWgs (backward, which also writes a partial row per workgroup)
+// workgroups per compute unit, after which the groups stride over the rows.
+// Backward, 2M rows of 128: 3 per unit 533 us, 4 552 us, 2 567 us; where a
+// workgroup holds a whole row its registers allow two: 8191 rows of 4096 with
+// 2 per unit 57 + 7 us (partial rows), with 3 76 + 9 us, with 4 70 + 12 us.
+constexpr int kNormBwdWgs = 3;
 static int norm_wgs(int64_t rows, int gpw, bool bwd) {
-  const int64_t need = (rows + gpw - 1) / gpw, cap = (int64_t)kda_host::device_cus() * (bwd ? 4 : 8);
+  const int64_t need = (rows + gpw - 1) / gpw;
+  const int64_t cap = (int64_t)kda_host::device_cus() * (bwd ? (gpw == 1 ? 2 : kNormBwdWgs) : 8);
   return (int)std::max<int64_t>(1, std::min(need, cap));
 }
 
@@ -322,7 +355,7 @@ static hipError_t norm_t(NormArgs a, hipStream_t s, void* dw, void* db) {
   };
   hipError_t e = vec ? go(std::integral_constant<int, FV>()) : go(std::integral_constant<int, 1>());
   if (e != hipSuccess || !BWD || !a.part) return e;
-  hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.D + 15) / 16), dim3(256), 0, s, a.part, wgs, a.D, a.wbf, dw, db);
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.D + 15) / 16), dim3(512), 0, s, a.part, wgs, a.D, a.wbf, dw, db);
   return hipGetLastError();
 }
 
@@ -331,7 +364,7 @@ static hipError_t norm_t(NormArgs a, hipStream_t s, void* dw, void* db) {
 namespace kda_host {
 
 size_t norm_bwd_ws_bytes(int D) {
-  return (size_t)device_cus() * 4 * 2 * (size_t)D * sizeof(float);
+  return (size_t)device_cus() * kda::kNormBwdWgs * 2 * (size_t)D * sizeof(float);
 }
 
 hipError_t launch_norm(kda_dtype dt, int64_t rows, const kda_norm& p, const int32_t* cu, int N, int rpt,
