@@ -16,8 +16,8 @@
 //   dS0 = e^{G_last} dS + (e^G q~)^T dO - (e^G K)^T E
 // The gate's gradient (bf16 inputs; FP32's way is in kda_gdn_chunk_bwd.hip): scale
 // every state from token t on, and v_i and o_i for i >= t with it; nothing
-// changes but the decay into t. So dg_t = <S_T, dS_T> + sum_{i >= t} s_i over
-// the sequence's end T with s_i = <o_i, dO_i> - <v_i, dv_i>, two scalars per
+// changes but the decay into t. So dg_t = <S_T, dS_T> + sum_{t <= i < T} s_i for
+// any T > t with s_i = <o_i, dO_i> - <v_i, dv_i>, two scalars per
 // token that the scans form in FP32. What a token adds to its own output is in
 // both and is left out of both, so that every term carries the decay (and a
 // strongly decaying head's small dg keeps its digits):
@@ -572,6 +572,11 @@ namespace kda {
 // Workspace of a chunked call, in order: the varlen chunk table, then per
 // (chunk, value head): row factors and fragments, and for the backward S0, Y,
 // dS, D, the per-token scalars of each 16 columns and the gate-parameter partials.
+constexpr int kGdnAnchor = 16;  // chunks between a sequence's anchors of the gate's gradient
+// A chunk c of a sequence that starts at flat chunk c0 and has an anchor: its
+// slot (anchors are 16 chunks apart and a sequence's first chunk has none, so
+// no two share one).
+__host__ __device__ __forceinline__ size_t gdn_anchor(int64_t c0, int c) { return (size_t)((c0 + c) / kGdnAnchor); }
 template <typename T>
 struct GdnLayout {
   int* table;
@@ -585,6 +590,8 @@ struct GdnLayout {
   float* tokf;   // [..][V / 16][64]: the tokens' scalars from the forward run, per 16 columns
   float* tokr;   // [..][V / 16][64]: those from the reverse scan
   float* end;    // [N * HV][V / 16]: <S_T, dS_T> of the columns
+  float* anc;    // [anchors * HV][V / 16]: <S, dS> of the columns before an anchor chunk
+  float* ancS;   // [anchors * HV][V / 16][K / 16][64][4]: S there in FP32, as the accumulators lie
   float* par;    // [..][2]
   size_t bytes;
   GdnLayout(const kda_dims& d, bool varlen, void* ws, bool bwd) {
@@ -601,7 +608,7 @@ struct GdnLayout {
     scal = reinterpret_cast<float*>(take(n * kGdnScal * kC * sizeof(float)));
     frag = reinterpret_cast<T*>(take(n * (bwd ? GdnWs<T>::bwd : GdnWs<T>::fwd) * sizeof(T)));
     fragT = S0 = Y = dS = D = nullptr;
-    tokf = tokr = end = par = nullptr;
+    tokf = tokr = end = anc = ancS = par = nullptr;
     if (bwd) {
       fragT = reinterpret_cast<T*>(take(n * GdnWs<T>::bwd * sizeof(T)));
       S0 = reinterpret_cast<T*>(take(n * d.K * d.V * sizeof(T)));
@@ -611,6 +618,11 @@ struct GdnLayout {
       tokf = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
       tokr = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
       end = reinterpret_cast<float*>(take((size_t)d.N * d.HV * (d.V / 16) * sizeof(float)));
+      if (GdnWs<T>::kScanGate) {
+        const size_t na = (size_t)(mc / kGdnAnchor + 1) * d.HV;
+        anc = reinterpret_cast<float*>(take(na * (d.V / 16) * sizeof(float)));
+        ancS = reinterpret_cast<float*>(take(na * d.K * d.V * sizeof(float)));
+      }
       par = reinterpret_cast<float*>(take(n * 2 * sizeof(float)));
     }
     bytes = (size_t)(p - p0);

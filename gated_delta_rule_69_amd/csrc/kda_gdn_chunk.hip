@@ -329,7 +329,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
                 int T_, int H, int HV, const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag,
                 int write_final, bf16* __restrict__ o, float* ht, const bf16* __restrict__ dO,
                 const float* __restrict__ dht, bf16* __restrict__ ws_S0, bf16* __restrict__ ws_Y,
-                float* __restrict__ ws_tok, float* __restrict__ ws_end) {
+                float* __restrict__ ws_tok, float* __restrict__ ws_end, float* __restrict__ ws_anc) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   using L_ = GdnScanLds<K, NP, BWD>;
   using TT = TokTile<bf16, K>;
@@ -371,6 +371,12 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
     __builtin_amdgcn_s_setprio(2);  // ahead of an output wave on the same SIMD
     for (int it = 0; it < nc; ++it) {
       __syncthreads();
+      if (BWD && it > 0 && it % kGdnAnchor == 0) {
+        float4* a = reinterpret_cast<float4*>(ws_anc) +
+                    ((gdn_anchor(ch.c0, it) * HV + hv) * (V / 16) + (col0 >> 4)) * RT * 64 + lane;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) a[r * 64] = make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
+      }
       const char* b = smem + (it & 1) * L_::sbuf;
       const bf16* sM = reinterpret_cast<const bf16*>(b + L_::sM);
       const float* sf = reinterpret_cast<const float*>(b + L_::sF);
@@ -894,7 +900,7 @@ static hipError_t scan_t(const kda_dims& d, const GdnCall& c, const GdnLayout<bf
   hipLaunchKernelGGL((gdn_scan_kernel<K, V, NP, BWD>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
                      dim3((BWD ? 256 : 128) * NP), lds, s, (const bf16*)c.q, (const bf16*)c.k, (const bf16*)c.v, c.h0, c.cu,
                      w.table, d.N, d.T, d.H, d.HV, w.scal, w.frag, c.ht != nullptr, (bf16*)c.o, c.ht,
-                     (const bf16*)c.dO, c.dht, w.S0, w.Y, w.tokf, w.end);
+                     (const bf16*)c.dO, c.dht, w.S0, w.Y, w.tokf, w.end, w.ancS);
   return hipGetLastError();
 }
 template <int K, int V, int NP, bool BWD>

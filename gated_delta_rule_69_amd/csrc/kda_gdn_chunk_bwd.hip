@@ -6,7 +6,7 @@
 //                         dv, its part of the tokens' scalars, and per chunk dS
 //                         (at the chunk's end) and D.
 //   gdn_gate_bwd_kernel   bf16: the gate's gradient from the tokens' scalars,
-//                         one workgroup per chain.
+//                         a workgroup per anchor.
 //   gdn_local_kernel      per (chunk, q/k head): dq, dk (summed over the head's
 //                         value heads) and dbeta from the chunk's S0, Y, dS and
 //                         D (gdn_local32_kernel for FP32 inputs, with the gate's
@@ -21,11 +21,15 @@
 // feed dq, dk and dbeta, which are rounded to it as well.
 //
 // The gate's gradient comes one of two ways.
-//   bf16: dg_t = <S_T, dS_T> + sum_{i >= t} s_i over the sequence (kda_gdn.h), from
-//     FP32 values inside the scans, summed in double. Formed from the rounded S0, Y, dS and D instead it was off by 2e-3, and
-//     dA_log and d_dt_bias, which sum it over tokens of either sign, by 1e-2
-//     and more. What is left (1e-6 of a token's two scalars, adding up like a
-//     random walk over the sequence) is far below bf16.
+//   bf16: dg_t = <S_T, dS_T> + sum_{t <= i < T} s_i (kda_gdn.h), from FP32 values
+//     inside the scans, summed in double. Formed from the rounded S0, Y, dS and D
+//     instead it was off by 2e-3, and dA_log and d_dt_bias, which sum it over
+//     tokens of either sign, by 1e-2 and more. A token's scalars are off by some
+//     1e-6, adding up like a random walk towards T, the same for all tokens
+//     before: with T the sequence's end dA_log was off by 5e-3 at 4096 tokens
+//     and 4e-2 at 16384. T is therefore the next anchor: every 16 chunks the
+//     forward run keeps S in FP32 and the reverse scan takes <S, dS> there (3%
+//     of the workspace).
 //   FP32: the operands are exact, the walk would not be small enough, and dg is
 //     taken chunk by chunk: what the decay between tokens t - 1 and t scales is
 //     the rows i >= t against S0, the columns j < t towards the chunk's end and
@@ -82,7 +86,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
                     const int* __restrict__ table, int N, int T_, int H, int HV,
                     const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag, bf16* __restrict__ dv,
                     float* __restrict__ dh0, bf16* __restrict__ ws_dS, bf16* __restrict__ ws_D,
-                    float* __restrict__ ws_tok) {
+                    float* __restrict__ ws_tok, const float* __restrict__ ws_ancS, float* __restrict__ ws_anc) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   using L_ = GdnRevLds<K, NP>;
   using TT = TokTile<bf16, K>;
@@ -124,6 +128,20 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     __builtin_amdgcn_s_setprio(2);
     for (int c = nc - 1, buf = 0; c >= 0; --c, buf ^= 1) {
       __syncthreads();
+      if (c + 1 < nc && (c + 1) % kGdnAnchor == 0) {  // <S, dS> before chunk c + 1
+        const size_t at = (gdn_anchor(ch.c0, c + 1) * HV + hv) * (V / 16) + (col0 >> 4);
+        const float4* a = reinterpret_cast<const float4*>(ws_ancS) + at * RT * 64 + lane;
+        float y = 0.f;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const float4 s = a[r * 64];
+          y += s.x * S[r][0] + s.y * S[r][1] + s.z * S[r][2] + s.w * S[r][3];
+        }
+        y = row16_sum(y);
+        y += __shfl_xor(y, 16);
+        y += __shfl_xor(y, 32);
+        if (lane == 0) ws_anc[at] = y;
+      }
       const char* b = smem + buf * L_::sbuf;
       const bf16* sM = reinterpret_cast<const bf16*>(b + L_::sM);
       const float* sf = reinterpret_cast<const float*>(b + L_::sF);
@@ -425,16 +443,18 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
   }
 }
 
-// bf16: the gate's gradient from the tokens' scalars, one workgroup per chain:
-// 16 chunks a step from the chain's end, lane = token, wave = chunk; the sums
-// towards the end are held in double.
+// bf16: the gate's gradient from the tokens' scalars. A workgroup takes the 16
+// chunks from one anchor to the next, lane = token, wave = chunk; the sums
+// towards the anchor behind them (the sequence's end for the last) are held in
+// double. Grid (chain, y): y strides over a chain's anchors.
 template <int V>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(64 * kGdnAnchor)
 gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __restrict__ table, int T_, int HV,
                     int has_h0, int has_dht, const float* __restrict__ tokf, const float* __restrict__ tokr,
-                    const float* __restrict__ ends, void* __restrict__ dgate, float* __restrict__ par) {
+                    const float* __restrict__ ends, const float* __restrict__ anc, void* __restrict__ dgate,
+                    float* __restrict__ par) {
   constexpr int NB = V / 16;
-  __shared__ double s_tot[2][16];
+  __shared__ double s_tot[2][kGdnAnchor];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = blockIdx.x / HV, hv = blockIdx.x % HV;
   int64_t bos = (int64_t)n * T_;
@@ -446,32 +466,24 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
   const int nc = (len + kC - 1) / kC;
   if (nc <= 0) return;
   const int64_t c0 = cu ? table[1 + n] : (int64_t)n * nc;
-  double tail = 0.;  // what lies behind the step's chunks
-  if (has_dht)
-    for (int i = 0; i < NB; ++i) tail += (double)ends[((size_t)n * HV + hv) * NB + i];
-  const float as = gate.raw && gate.A_log ? expf(ld_any(gate.A_log, hv, gate.bf)) : 1.f;
-  const float bias = gate.raw && gate.dt_bias ? ld_any(gate.dt_bias, hv, gate.bf) : 0.f;
-  float x[NB], y[NB], gx = 0.f;
-  auto fetch = [&](int c) __attribute__((always_inline)) {
-    const size_t at = (size_t)((c0 + max(c, 0)) * HV + hv) * NB * kC + lane;
-#pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      x[i] = tokf[at + i * kC];
-      y[i] = tokr[at + i * kC];
-    }
-    const int t = min(max(c, 0) * kC + lane, len - 1);
-    gx = ld_any(gate.x, (bos + t) * HV + hv, gate.bf);
-  };
-  fetch(nc - 1 - wave);
-  for (int top = nc, b = 0; top > 0; top -= 16, b ^= 1) {
-    const int c = top - 1 - wave;
-    const bool ok = c >= 0 && lane < min(kC, len - c * kC);
+  for (int m = blockIdx.y, b = 0; m * kGdnAnchor < nc; m += gridDim.y, b ^= 1) {
+    const int c = m * kGdnAnchor + wave, cl = min(c, nc - 1);
+    const bool ok = c < nc && lane < len - c * kC;
+    const size_t at = (size_t)((c0 + cl) * HV + hv) * NB * kC + lane;
+    const int64_t tok = (bos + min(cl * kC + lane, len - 1)) * HV + hv;
     double s = 0.;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) s += (double)x[i] - (double)y[i];
+    for (int i = 0; i < NB; ++i) s += (double)tokf[at + i * kC] - (double)tokr[at + i * kC];
     if (!ok) s = 0.;
-    const float xb = gate.dt_bias ? gx + bias : gx;
-    if (top > 16) fetch(c - 16);
+    const bool last = (m + 1) * kGdnAnchor >= nc;
+    const float* e = last ? ends + ((size_t)n * HV + hv) * NB
+                          : anc + (gdn_anchor(c0, (m + 1) * kGdnAnchor) * HV + hv) * NB;
+    double behind = 0.;
+    if (!last || has_dht)
+#pragma unroll
+      for (int i = 0; i < NB; ++i) behind += (double)e[i];
+    float xb, as;
+    const float gn = gdn_gate(gate, tok, hv, &xb, &as);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const double z = __shfl_down(s, d);
@@ -479,26 +491,15 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
     }
     if (lane == 0) s_tot[b][wave] = s;
     __syncthreads();
-    double behind = tail;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) {
-      const double z = s_tot[b][w];
-      if (w < wave) behind += z;
-      tail += z;
-    }
-    if (c < 0) continue;
+    for (int w = kGdnAnchor - 1; w > 0; --w) behind += w > wave ? s_tot[b][w] : 0.;
+    if (c >= nc) continue;
     // before a sequence's first token there is nothing to decay without a state
     const float dg = c == 0 && lane == 0 && !has_h0 ? 0.f : (float)(s + behind);
-    float pa = 0.f, pb = 0.f;
-    if (ok) {
-      const int64_t at = (bos + (int64_t)c * kC + lane) * HV + hv;
-      const float gn = gate.raw ? -as * softplus_f32(xb) : xb;
-      const float dx = gate.raw ? -dg * as * sigmoid_f32(xb) : dg;
-      st_any(dgate, at, gate.bf, dx);
-      pa = dg * gn;  // dg / dA_log = g
-      pb = dx;
-    }
+    const float dx = gate.raw ? -dg * as * sigmoid_f32(xb) : dg;
+    if (ok) st_any(dgate, tok, gate.bf, dx);
     if (gate.A_log || gate.dt_bias) {
+      float pa = ok ? dg * gn : 0.f, pb = ok ? dx : 0.f;  // dg / dA_log = g
 #pragma unroll
       for (int d = 32; d; d >>= 1) {
         pa += __shfl_xor(pa, d);
@@ -1337,7 +1338,7 @@ static hipError_t rev_t(const kda_dims& d, const void* q, const void* k, const v
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((gdn_rev_scan_kernel<K, V, NP>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
                      dim3(256 * NP), lds, s, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)dO, dht,
-                     cu, w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (bf16*)dv, dh0, w.dS, w.D, w.tokr);
+                     cu, w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (bf16*)dv, dh0, w.dS, w.D, w.tokr, w.ancS, w.anc);
   return hipGetLastError();
 }
 template <int K, int V, int NP>
@@ -1359,8 +1360,11 @@ template <int K, int V>
 static hipError_t local_t(const kda_dims& d, const void* q, const void* k, const void* dO, const GdnGate& gate, int l2,
                           int has_h0, int has_dht, const int32_t* cu, const GdnLayout<bf16>& w, void* dq, void* dk,
                           void* dbeta, void* dgate, hipStream_t s) {
-  hipLaunchKernelGGL((gdn_gate_bwd_kernel<V>), dim3((unsigned)(d.N * d.HV)), dim3(1024), 0, s, gate, cu, w.table, d.T,
-                     d.HV, has_h0, has_dht, w.tokf, w.tokr, w.end, dgate, w.par);
+  const int64_t mc = max_chunks(d, cu != nullptr);
+  const int64_t chains = (int64_t)d.N * d.HV, segs = (cu ? mc : mc / d.N) / kGdnAnchor + 1;
+  const int64_t ny = std::min<int64_t>(segs, std::max<int64_t>(1, 4 * kda_host::device_cus() / chains));
+  hipLaunchKernelGGL((gdn_gate_bwd_kernel<V>), dim3((unsigned)chains, (unsigned)ny), dim3(64 * kGdnAnchor), 0, s, gate,
+                     cu, w.table, d.T, d.HV, has_h0, has_dht, w.tokf, w.tokr, w.end, w.anc, dgate, w.par);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr size_t lds = GdnLocalLds<K, V>::total;
@@ -1368,7 +1372,6 @@ static hipError_t local_t(const kda_dims& d, const void* q, const void* k, const
   e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gdn_local_kernel<K, V>),
                           hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
-  const int64_t mc = max_chunks(d, cu != nullptr);
   const int64_t wgs = std::min<int64_t>(mc * d.H, kda_host::device_cus());
   hipLaunchKernelGGL((gdn_local_kernel<K, V>), dim3((unsigned)wgs), dim3(512), lds, s, (const bf16*)q, (const bf16*)k,
                      (const bf16*)dO, cu, w.table, (int)mc, d.N, d.T, d.H, d.HV, l2, 1.0f / sqrtf((float)K), w.scal,
