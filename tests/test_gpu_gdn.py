@@ -392,3 +392,35 @@ def test_random_shapes(seed):
     _check_fwd(c)
     _check_bwd(c)
     _check_fwd(c, kda.recurrent_gdn)
+
+
+def test_backward_across_many_chunks():
+    """Sequences of 16 chunks and one token less and more, and of two such
+    stretches: where the gate's gradient is summed from another point."""
+    _check_bwd(G.make(44, [1025, 1024, 1023, 2113, 5, 0], H=1, HV=2))
+    _check_bwd(G.make(45, [1100, 1100], dense=True, H=1, HV=1, K=128, V=128, step=(1e-4, 1e-2)))
+
+
+@pytest.mark.parametrize("lens,H,HV,K", [([16384], 1, 2, 128), ([9000, 7000], 2, 2, 64), ([2200] + [1] * 19, 1, 64, 64)])
+def test_long_backward_agrees_with_fp32(lens, H, HV, K):
+    """bf16 gradients of long sequences against the FP32 kernels' on the same
+    values (those are within 2e-5 of FP64 in the tests above): the parameters'
+    gradients sum 16384 tokens of either sign, where an error that every token
+    of a stretch shares would show. The last case has more chains than the
+    kernel over them has workgroups."""
+    for seed in (70, 71, 72):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        r = lambda *s: torch.randn(*s, device=DEV, generator=g).bfloat16()  # noqa: E731
+        T = sum(lens)
+        q, k, v, do = r(1, T, H, K), r(1, T, H, K), r(1, T, HV, K), r(1, T, HV, K)
+        x, beta = r(1, T, HV), torch.sigmoid(r(1, T, HV))
+        A = torch.linspace(0, 2.5, HV, device=DEV).bfloat16()
+        b = torch.linspace(-6, -2, HV, device=DEV).bfloat16()
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=DEV)
+        res = [kda.chunk_gdn_bwd(*(a.to(t) for a in (q, k, v, x, beta)), None, do.to(t), None, cu_seqlens=cu,
+                                 use_gate_in_kernel=True, A_log=A.to(t), dt_bias=b.to(t), qk_l2norm=True)
+               for t in (torch.bfloat16, torch.float32)]
+        for m in ("dq", "dk", "dv", "dg", "dbeta", "dA_log", "ddt_bias"):
+            e = G.rel(res[0][m], res[1][m].cpu().numpy())
+            assert e <= (DV16 if m == "dv" else G16), (seed, m, e)
