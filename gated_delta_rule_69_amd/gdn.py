@@ -17,7 +17,13 @@ from typing import Optional, Tuple
 import torch
 
 from . import (KDA_BF16, KDA_FP32, KDA_GATE_NAT, KDA_GATE_RAW, KdaDims, KdaError, _cu_dims, _I32_MAX, _lib,
-               _nbytes, _ptr)
+               _nbytes)
+
+
+def _ptr(t):
+    """A tensor's address (None passes): what a c_void_p argument takes."""
+    return None if t is None else t.data_ptr()
+
 
 _DT = {torch.bfloat16: KDA_BF16, torch.float32: KDA_FP32}
 
@@ -28,17 +34,26 @@ class KdaGdnGate(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32)]
 
 
+def _stream_of(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same handle without a Stream object around it: 0.1 instead of 2.8 us, of
+# a single-token call's 12
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_of)
+
+
 class _OnDevice:
     """Makes a tensor's device the current one for the call (stream, launch)."""
 
     def __init__(self, t: torch.Tensor):
-        self._index = t.device.index
+        self._index = t.get_device()
 
     def __enter__(self):
         self._old = torch.cuda.current_device()
         if self._old != self._index:
             torch.cuda.set_device(self._index)
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return _stream_of(self._index)
 
     def __exit__(self, *exc):
         if self._old != self._index:
@@ -47,7 +62,8 @@ class _OnDevice:
 
 def _want(t, name, shape, dtype, device):
     """A contiguous tensor of exactly this shape, dtype and device (None passes)."""
-    if t is None:
+    if t is None or (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+                     and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -197,9 +213,9 @@ def recurrent_gdn(q, k, v, gate, beta, initial_state=None, *, cu_seqlens=None, o
     and short sequences. Arguments as chunk_gdn; pass final_state=initial_state
     to update the states in place. Inference only: inputs that require grad are
     rejected (use chunk_gdn for training)."""
-    if any(isinstance(t, torch.Tensor) and t.requires_grad
-           for t in (q, k, v, gate, beta, initial_state, A_log, dt_bias)):
-        raise RuntimeError("recurrent_gdn is inference-only; inputs require grad (use chunk_gdn)")
+    for t in (q, k, v, gate, beta, initial_state, A_log, dt_bias):
+        if isinstance(t, torch.Tensor) and t.requires_grad:
+            raise RuntimeError("recurrent_gdn is inference-only; inputs require grad (use chunk_gdn)")
     d, g = _check_args(q, k, v, gate, beta, initial_state, cu_seqlens, use_gate_in_kernel, A_log, dt_bias, o,
                        final_state)
     if o is None:

@@ -13,8 +13,8 @@ from typing import Optional
 
 import torch
 
-from . import KdaError, _cu_dims, _lib, _nbytes, _ptr
-from .gdn import _DT, _OnDevice, _want, _workspace
+from . import KdaError, _cu_dims, _lib, _nbytes
+from .gdn import _DT, _OnDevice, _ptr, _want, _workspace
 
 _KINDS = {"rms": 0, "layer": 1}
 _ACTS = {"silu": 0, "sigmoid": 1}
