@@ -1,6 +1,7 @@
 // C ABI of libkda: argument validation, then kernel launches on the caller's stream.
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "kda_common.h"
@@ -631,8 +632,12 @@ kda_status gdn_gate_args(const kda_dims* d, kda_dtype dt, const kda_gdn_gate* g,
 
 bool gdn_chunk_supported(const kda_dims* d) {
   // 64 tokens' rows of q or v span less than 2^31 bytes (the kernels' 32-bit offsets)
-  return (d->K == 64 || d->K == 128) && (d->V == 64 || d->V == 128) &&
-         (int64_t)d->H * d->K < (1 << 23) && (int64_t)d->HV * d->V < (1 << 23);
+  if ((d->K != 64 && d->K != 128) || (d->V != 64 && d->V != 128)) return false;
+  if ((int64_t)d->H * d->K >= (1 << 23) || (int64_t)d->HV * d->V >= (1 << 23)) return false;
+  // the grids' threads fit 32 bits: at most 512 per 32 columns of a (sequence,
+  // value head), 1024 per 64, 256 per (chunk, value head)
+  const int64_t chunks = (int64_t)std::max(d->B, 1) * (((int64_t)d->T + 63) / 64) + d->N;
+  return (int64_t)d->N * d->HV * d->V < (1 << 28) - 8 * 128 && chunks < (1 << 24) / std::max(d->HV, 1);
 }
 
 // Buffers of one call: every output is checked against every input and every
@@ -757,6 +762,8 @@ kda_status kda_gdn_recurrent_fwd(const kda_dims* d, kda_dtype dt, const void* q,
   kda_status st = gdn_check_fwd(d, dt, q, k, v, gate, beta, h0, cu, write_final, o, ht, nullptr, 0, &gg);
   if (st != KDA_OK) return st;
   if (d->K > 256 || d->V > 256) return KDA_ERR_UNSUPPORTED;
+  // the grid's threads fit 32 bits: at most 64 per 16 columns of a (sequence, value head)
+  if ((int64_t)d->N * d->HV >= (1 << 26) / ((d->V + 15) / 16)) return KDA_ERR_UNSUPPORTED;
   return kda_host::launch_gdn_recurrent(*d, dt, q, k, v, gg, l2 != 0, beta, h0, cu, write_final != 0, o, ht,
                                         stream) == hipSuccess
              ? KDA_OK

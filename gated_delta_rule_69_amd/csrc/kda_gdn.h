@@ -308,8 +308,9 @@ __device__ __forceinline__ void tile_st(float* p, uint32_t stride, int row4, int
 // into memory in operand order: [r][block s of 32 columns][lane][8], so that a
 // later kernel's lane reads its eight column elements of row l16 as one 16-byte
 // piece and a wave 1 KB in one go, with rows or columns as the product's rows
-// alike. The bf16 tile is 512 consecutive bytes. (Row by row instead, 32 bytes
-// per row and wave: local kernel 362 us against 305, reverse scan 374 against 365.)
+// alike. The bf16 tile is 512 consecutive bytes. (Row by row, 32 bytes per row
+// and wave, the kernels of that time took 362 us against 305, local, and 374
+// against 365, reverse scan.)
 __device__ __forceinline__ void op_st(bf16* p, int r, int cb, int nv, uint2 x) {  // x: packed accumulator
   const int lane = threadIdx.x & 63, g = lane >> 4, Q = (lane >> 2) & 3, q = lane & 3;
   bf16* d = p + (r * nv + (cb >> 1)) * kFragElems;

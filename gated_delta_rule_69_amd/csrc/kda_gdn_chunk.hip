@@ -302,12 +302,16 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
 // about 1000 instructions of one wave with nothing else on its SIMD (2.5 us of
 // 3.9 us per chunk at 64 chains); the two halves of the work now run on two.
 // Two barriers per chunk: at its top (operands in LDS) and after the output
-// wave has taken the previous chunk's S and Y.
+// wave has taken the previous chunk's S and Y. What bounds it now is the step
+// of the recurrence, 2.1 us a chunk with 32 columns per workgroup (64 chains
+// of 4096 tokens, K = V = 128: 135 us) and 3.4 us with 64, where state and
+// output waves share their SIMDs' issue slots (608 chains, 32768 tokens: 431 us).
 //
 // BWD: the backward's run over the forward. S0 and Y are kept instead of O, and
 // dO comes in: o' is formed in full precision (S0 and P split as well; P is
 // strictly lower) for the tokens' scalars of the gate's gradient. A third wave
-// per pair stores S0 and Y (of 4 NP waves, NP leave at once).
+// per pair stores S0 and Y (of 4 NP waves, NP leave at once): 64 chains of 4096
+// tokens 245 us (261 us with the output wave storing them).
 template <int K, int NP, bool BWD>
 struct GdnScanLds {
   static constexpr int NK = K / 32, PT = BWD ? 2 : 1;
@@ -926,7 +930,9 @@ static hipError_t gdn_fwd_kv(const kda_dims& d, const GdnCall& c, void* ws, hipS
   }
   if (mc > 0) {
     // all value heads of a q/k head in one workgroup (q k^T and k k^T formed
-    // once) as long as that leaves two workgroups per compute unit
+    // once) as long as that leaves two workgroups per compute unit (two value
+    // heads a head: 32768 tokens x 16 heads 199 us, one workgroup each 239 us;
+    // 8 chunks x 2 heads, FP32, 19 and 12 us)
     const int grp = d.HV / d.H;
     const int hpw = mc * d.H >= 2 * (int64_t)kda_host::device_cus() ? grp : 1;
     hipLaunchKernelGGL((gdn_intra_kernel<T, K, BWD>), dim3((unsigned)(mc * (d.HV / hpw))), dim3(256), 0, s,
@@ -935,8 +941,10 @@ static hipError_t gdn_fwd_kv(const kda_dims& d, const GdnCall& c, void* ws, hipS
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  // 64 columns per workgroup while that fills the device, else 32
-  // (the backward's exchange of 64 columns does not fit LDS)
+  // 64 columns per workgroup while that fills the device, else 32 (608 chains
+  // of V = 128, 32768 tokens: 64 columns 431 us, 32 columns 575 us; 64 chains of
+  // 4096 tokens: 188 and 135 us). The backward's exchange of 64 columns does
+  // not fit LDS.
   const bool wide = (int64_t)d.N * d.HV * (V / 64) >= kda_host::device_cus();
   if constexpr (!BWD || sizeof(T) == 4) {
     if (wide) return scan_t<K, V, 4, BWD>(d, c, w, s);

@@ -54,7 +54,8 @@ namespace kda {
 // chains.) Two barriers per chunk: at its top (operands, p and Z in LDS), and
 // after the state wave has taken p and Z and the behind wave the previous
 // chunk's dS and D'. Of the workgroup's 4 NP waves NP leave at once: the state
-// waves then have a SIMD each, ahead and behind waves share the others.
+// waves then have a SIMD each, ahead and behind waves share the others. 64
+// chains of 4096 tokens, K = V = 128: 246 us, 3.8 us a chunk, bound by the step.
 template <int K, int NP>
 struct GdnRevLds {
   static constexpr int NK = K / 32, RT = K / 16;
@@ -676,7 +677,8 @@ __device__ __forceinline__ float op_dot(const Op8<T>& a, const Op8<T>& b) {
 // workgroup stays on a CU, walks its (chunk, head) items and keeps two sets of
 // transfers into LDS going: S0, dS, k and q arrive while the 64 x 64 products
 // run over Y, D and dO, and the next item's Y, D and dO while the channel tiles
-// run over S0 and dS.
+// run over S0 and dS. 4096 items of K = V = 128, 720 MB: 175 us, 4.1 TB/s (305 us
+// with four waves a workgroup loading their operands where they use them).
 template <int K, int V>
 struct GdnLocalLds {
   static constexpr uint32_t tok = TokTile<bf16, K>::bytes, st = K * V * sizeof(bf16), row = kC * V * sizeof(bf16);
@@ -998,7 +1000,9 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
   }
 }
 
-// FP32. Four waves, one per token tile, operands straight from memory.
+// FP32. Four waves, one per token tile, operands straight from memory. With few
+// chunks (8 x 2 heads, K = 64, V = 128: 65 us) the FP32 matrix cores of a few
+// compute units bound it: eight waves split as above took 63 us.
 template <int K, int V>
 __global__ void __launch_bounds__(256)
 gdn_local32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ dO, GdnGate gate,

@@ -549,7 +549,8 @@ typedef struct {
 } kda_gdn_gate;
 
 /* Workspace bytes of kda_gdn_chunk_fwd (backward 0) or kda_gdn_chunk_bwd
- * (backward 1). 0 on invalid or unsupported dims (K and V in {64, 128}). */
+ * (backward 1). 0 on invalid or unsupported dims (K and V in {64, 128}; H K and
+ * HV V below 2^23, N HV V below 2^28, chunks x HV below 2^24). */
 size_t kda_gdn_chunk_workspace_bytes(const kda_dims* dims, kda_dtype dtype, int32_t backward);
 
 /*

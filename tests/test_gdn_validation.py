@@ -192,3 +192,15 @@ def test_abi_norm_backward_refusals():
     assert _norm_b(w=P[5].value, dw=P[6], ws=ctypes.c_void_p(P[9].value + 4)) == 4
     assert _norm_b(w=P[5].value, dw=P[2]) == 5
     assert _norm_b(z=P[7], dz=P[2]) == 5
+
+
+def test_abi_sizes_past_the_grids():
+    """Sizes whose grids would not fit are refused, not wrapped around."""
+    lib = kda.load()
+    for kw in (dict(N=1 << 22), dict(N=1, T=(1 << 30), HV=1 << 10, H=1 << 10), dict(H=1 << 17, HV=1 << 17),
+               dict(N=(1 << 31) - 1, T=(1 << 31) - 1, HV=1 << 16, H=1 << 16)):
+        for dt in (0, 1):
+            assert lib.kda_gdn_chunk_workspace_bytes(ctypes.byref(_dims(**kw)), dt, 1) == 0, kw
+    assert lib.kda_gdn_chunk_workspace_bytes(ctypes.byref(_dims(N=1 << 15, T=1 << 17, H=16, HV=32)), 1, 1) > 0
+    assert _fwd(_dims(N=1 << 22), _gate(), cu=P[9], fin=0) == 4
+    assert _rec(_dims(N=1 << 26, V=4), _gate(), cu=P[9], fin=0) == 4
