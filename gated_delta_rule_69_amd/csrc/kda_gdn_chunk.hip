@@ -309,9 +309,9 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
 //
 // BWD: the backward's run over the forward. S0 and Y are kept instead of O, and
 // dO comes in: o' is formed in full precision (S0 and P split as well; P is
-// strictly lower) for the tokens' scalars of the gate's gradient. A third wave
-// per pair stores S0 and Y (of 4 NP waves, NP leave at once): 64 chains of 4096
-// tokens 245 us (261 us with the output wave storing them).
+// strictly lower) for the tokens' scalars of the gate's gradient. Two output waves
+// per pair take two token tiles each, and a fourth wave stores S0 and Y: 64
+// chains of 4096 tokens 200 us (one output wave 245 us, storing too 261 us).
 template <int K, int NP, bool BWD>
 struct GdnScanLds {
   static constexpr int NK = K / 32, PT = BWD ? 2 : 1;
@@ -341,9 +341,8 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
   constexpr size_t kFrag = BWD ? GdnWs<bf16>::bwd : GdnWs<bf16>::fwd;
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pair = wave % NP, role = wave / NP;  // 0 state, 1 output, 3 store
+  const int pair = wave % NP, role = wave / NP;  // 0 state, 1 output (BWD: and 3), 2 store
   const bool state_wave = role == 0;
-  if (role == 2) return;
   const GdnChain ch = gdn_chain(NVB, cu, table, N, T_, H, HV);
   if (!ch.ok) return;
   const int col0 = ch.vb * BV + 16 * pair, hv = ch.hv, len = ch.len;
@@ -550,7 +549,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
   }
 
   if constexpr (BWD) {
-    if (role == 3) {  // S0 (its high part) and Y of the chunk behind
+    if (role == 2) {  // S0 (its high part) and Y of the chunk behind
       __syncthreads();
       for (int it = 0; it <= nc; ++it) {
         __syncthreads();
@@ -575,40 +574,42 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
     }
   }
 
-  // ---- output wave
+  // ---- output wave: all four token tiles, BWD tiles 0, 1 or 2, 3
+  constexpr int OT = BWD ? 2 : 4, NO = BWD ? 2 * NP : NP;
+  const int t0 = BWD && role == 3 ? 2 : 0, ow = BWD && role == 3 ? NP + pair : pair;
   const uint32_t lds = lds_addr(smem);
-  const TokDma<bf16, K, NP> tok((uint32_t)(H * K * sizeof(bf16)), pair);
+  const TokDma<bf16, K, NO> tok((uint32_t)(H * K * sizeof(bf16)), ow);
   auto fetch_s = [&](int c) __attribute__((always_inline)) {  // what the state waves read
     const uint32_t b = lds + (c & 1) * L_::sbuf;
     tok.go(b, k + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
-    dma_flat<2 * L_::tri, NP>(b + L_::sM, ws_frag + chunk(c) * kFrag, pair);
-    dma_flat<L_::scal, NP>(b + L_::sF, ws_scal + chunk(c) * (kGdnScal * kC), pair);
+    dma_flat<2 * L_::tri, NO>(b + L_::sM, ws_frag + chunk(c) * kFrag, ow);
+    dma_flat<L_::scal, NO>(b + L_::sF, ws_scal + chunk(c) * (kGdnScal * kC), ow);
   };
   auto fetch_o = [&](int c) __attribute__((always_inline)) {  // what the output waves read
     const uint32_t b = lds + L_::at_o + (c & 1) * L_::obuf;
     tok.go(b, q + ((ch.bos + (int64_t)c * kC) * H + ch.h) * K, tokens(c));
-    dma_flat<L_::PT * L_::tri, NP>(b + L_::oP, ws_frag + chunk(c) * kFrag + 2 * kTriElems, pair);
-    dma_flat<L_::scal, NP>(b + L_::oF, ws_scal + chunk(c) * (kGdnScal * kC) + kSb * kC, pair);
+    dma_flat<L_::PT * L_::tri, NO>(b + L_::oP, ws_frag + chunk(c) * kFrag + 2 * kTriElems, ow);
+    dma_flat<L_::scal, NO>(b + L_::oF, ws_scal + chunk(c) * (kGdnScal * kC) + kSb * kC, ow);
   };
-  TileRaw<bf16> dr[4];
+  TileRaw<bf16> dr[OT];
   fetch_s(0);
   lds_dma_wait();
   __syncthreads();
   for (int it = 0; it <= nc; ++it) {
-    // behind the previous round's transfers: the 4 stores of chunk it - 2, a full one
-    if (it >= 2) lds_dma_wait_but<4>();
+    // behind the previous round's transfers: the OT stores of chunk it - 2, a full one
+    if (it >= 2) lds_dma_wait_but<OT>();
     else lds_dma_wait();
     __syncthreads();
     if constexpr (BWD) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < OT; ++t)
         if (it > 0) settle(dr[t].r);
     }
     if (it + 1 < nc) fetch_s(it + 1);
     if (it < nc) fetch_o(it);
     const int c = it - 1;
     Op8s<bf16> sb[NK];
-    f32x4 x[4], pred[4], dot[4];
+    f32x4 x[4], pred[OT], dot[OT];
     if (it > 0) {
 #pragma unroll
       for (int s = 0; s < NK; ++s) {
@@ -618,14 +619,18 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         x[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + (t * 64 + lane) * 16);
-        if constexpr (BWD) pred[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + L_::xY + (t * 64 + lane) * 16);
+      }
+      if constexpr (BWD) {
+#pragma unroll
+        for (int t = 0; t < OT; ++t)
+          pred[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + L_::xY + ((t0 + t) * 64 + lane) * 16);
       }
     }
     __syncthreads();
     if (it == 0) {
       if constexpr (BWD) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) tile_ld(dr[t], dO + vrow(0), HV * V, perm_row4(t, g), col0, tokens(0));
+        for (int t = 0; t < OT; ++t) tile_ld(dr[t], dO + vrow(0), HV * V, perm_row4(t0 + t, g), col0, tokens(0));
       }
       continue;
     }
@@ -634,25 +639,25 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
     const float* sf = reinterpret_cast<const float*>(b + L_::oF);  // from slot kSb on
     if constexpr (BWD) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) dot[t] = tile_get(dr[t]);
+      for (int t = 0; t < OT; ++t) dot[t] = tile_get(dr[t]);
       if (it < nc) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) tile_ld(dr[t], dO + vrow(it), HV * V, perm_row4(t, g), col0, tokens(it));
+        for (int t = 0; t < OT; ++t) tile_ld(dr[t], dO + vrow(it), HV * V, perm_row4(t0 + t, g), col0, tokens(it));
       }
     }
     // O = e^G q~ S0 + P Delta, Delta = b Y
-    Op8<bf16> qa[2][4], pf[L_::PT][6];
-    f32x4 qs[4];
+    Op8<bf16> qa[2][OT], pf[L_::PT][BWD ? 4 : 6];
+    f32x4 qs[OT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) qs[t] = zero4();
+    for (int t = 0; t < OT; ++t) qs[t] = zero4();
     auto read_q = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) TT::rows(qa[s & 1][t], b, t, s);
+      for (int t = 0; t < OT; ++t) TT::rows(qa[s & 1][t], b, t0 + t, s);
     };
     read_q(0);
     float bb[4][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) lds4(sf +  perm_row4(t, g), bb[t]);
+    for (int t = 0; t < 4; ++t) lds4(sf + perm_row4(t, g), bb[t]);
     Op8s<bf16> db[2];  // split: with S0 and P rounded as well, hi alone left o at 1.65x its rounding error
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -663,6 +668,11 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
         for (int e = 0; e < 4; ++e) d[i][e] = bb[2 * s + i][e] * x[2 * s + i][e];
       make_op(db[s], d[0], d[1]);
     }
+    // BWD: P's fragments of the wave's tiles, [s][tile]: tiles 0, 1 have none at s = 1, and read
+    // others that the branch below leaves out
+    const auto frag = [&](int f) __attribute__((always_inline)) {
+      return BWD ? (t0 ? 2 + 2 * (f & 1) + (f >> 1) : f & 1) : f;
+    };
 #pragma unroll
     for (int s = 0; s < NK; ++s) {
       stage();
@@ -672,37 +682,54 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
 #pragma unroll
         for (int pt = 0; pt < L_::PT; ++pt)
 #pragma unroll
-          for (int f = 0; f < 6; ++f) ld_op(pf[pt][f], sP + pt * kTriElems + f * kFragElems + lane * 8);
+          for (int f = 0; f < (BWD ? 4 : 6); ++f)
+            ld_op(pf[pt][f], sP + pt * kTriElems + frag(f) * kFragElems + lane * 8);
       }
       stage();
       if constexpr (BWD) {
-        mma_rows(qa[s & 1], sb[s], qs);
+#pragma unroll
+        for (int t = 0; t < OT; ++t) qs[t] = mma8s(qa[s & 1][t], sb[s], qs[t]);
       } else {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) qs[t] = mma8h(qa[s & 1][t], sb[s], qs[t]);
+        for (int t = 0; t < OT; ++t) qs[t] = mma8h(qa[s & 1][t], sb[s], qs[t]);
       }
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < OT; ++t) {
       float f[4];
-      lds4(sf + (kSq - kSb) * kC + perm_row4(t, g), f);
+      lds4(sf + (kSq - kSb) * kC + perm_row4(t0 + t, g), f);
 #pragma unroll
       for (int e = 0; e < 4; ++e) qs[t][e] *= f[e];
     }
-    mma_tri<L_::PT>(pf, db, qs);
     if constexpr (BWD) {
+      auto mma_p = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < OT; ++t)
+          qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[0][2 * s + t].v, db[s].lo, qs[t], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < OT; ++t)
+          qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[1][2 * s + t].v, db[s].hi, qs[t], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < OT; ++t)
+          qs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[0][2 * s + t].v, db[s].hi, qs[t], 0, 0, 0);
+      };
+      if (t0) mma_p(1);
+      mma_p(0);
       float* tk = ws_tok + (chunk(c) * (V / 16) + (col0 >> 4)) * kC;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        float f[4], y[4];
-        lds4(sf + (kSp - kSb) * kC + perm_row4(t, g), f);
+      for (int t = 0; t < OT; ++t) {
+        const int row4 = perm_row4(t0 + t, g);
+        float f[4], y[4], w[4];
+        lds4(sf + (kSp - kSb) * kC + row4, f);
+        lds4(sf + row4, w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = row16_sum(dot[t][e] * (qs[t][e] - f[e] * bb[t][e] * pred[t][e]));
-        if (l16 == 0) *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = make_float4(y[0], y[1], y[2], y[3]);
+        for (int e = 0; e < 4; ++e) y[e] = row16_sum(dot[t][e] * (qs[t][e] - f[e] * w[e] * pred[t][e]));
+        if (l16 == 0) *reinterpret_cast<float4*>(tk + row4) = make_float4(y[0], y[1], y[2], y[3]);
       }
     } else {
+      mma_tri<L_::PT>(pf, db, qs);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) tile_st(o + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c), qs[t]);
+      for (int t = 0; t < OT; ++t) tile_st(o + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c), qs[t]);
     }
   }
 }

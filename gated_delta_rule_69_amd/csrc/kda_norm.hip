@@ -328,7 +328,7 @@ static hipError_t norm_pick(int D, Fn&& go) {
     KDA_NORM_CFG(256, 1)
     KDA_NORM_CFG(256, 2)
     KDA_NORM_CFG(256, 4)
-    KDA_NORM_CFG(256, 8)
+    if constexpr (sizeof(T) == 4) KDA_NORM_CFG(256, 8)  // 8192 columns; bf16 has them with 4 rounds of 8
   } else {
     KDA_NORM_CFG(16, 4)
     KDA_NORM_CFG(64, 4)
