@@ -311,11 +311,17 @@ __device__ __forceinline__ void tile_st(float* p, uint32_t stride, int row4, int
 // alike. The bf16 tile is 512 consecutive bytes. (Row by row, 32 bytes per row
 // and wave, the kernels of that time took 362 us against 305, local, and 374
 // against 365, reverse scan.)
-__device__ __forceinline__ void op_st(bf16* p, int r, int cb, int nv, uint2 x) {  // x: packed accumulator
+__device__ __forceinline__ uint32_t op_at() {  // a lane's four elements within a bf16 tile
   const int lane = threadIdx.x & 63, g = lane >> 4, Q = (lane >> 2) & 3, q = lane & 3;
-  bf16* d = p + (r * nv + (cb >> 1)) * kFragElems;
-  *reinterpret_cast<uint2*>(d + (uint32_t)(((2 * (cb & 1) + (Q >> 1)) * 16 + 4 * g + q) * 8 + 4 * (Q & 1))) =
+  return ((Q >> 1) * 16 + 4 * g + q) * 8 + 4 * (Q & 1);
+}
+__device__ __forceinline__ void op_st(bf16* p, int r, int cb, int nv, uint2 x) {  // x: packed accumulator
+  *reinterpret_cast<uint2*>(p + (r * nv + (cb >> 1)) * kFragElems + (cb & 1) * (kFragElems / 2) + op_at()) =
       quad_transpose(x);
+}
+// a tile as op_st wrote it (quad_transpose gives the packed accumulator)
+__device__ __forceinline__ uint2 op_tile_ld(const bf16* p, int r, int cb, int nv) {
+  return *reinterpret_cast<const uint2*>(p + (r * nv + (cb >> 1)) * kFragElems + (cb & 1) * (kFragElems / 2) + op_at());
 }
 __device__ __forceinline__ void op_st(float* p, int r, int cb, int nv, const f32x4& x) {
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
@@ -588,9 +594,11 @@ struct GdnLayout {
   T* Y;          // [..][64][V]
   T* dS;         // [..][K][V]
   T* D;          // [..][64][V]
+  T* Yl;         // bf16: Y's low part, [..][V / 16][4][64][4] as the accumulators lie
   float* tokf;   // [..][V / 16][64]: the tokens' scalars from the forward run, per 16 columns
   float* tokr;   // [..][V / 16][64]: those from the reverse scan
   float* end;    // [N * HV][V / 16]: <S_T, dS_T> of the columns
+  float* tokb;   // [..][V / 16][64]: <D, Y>
   float* anc;    // [anchors * HV][V / 16]: <S, dS> of the columns before an anchor chunk
   float* ancS;   // [anchors * HV][V / 16][K / 16][64][4]: S there in FP32, as the accumulators lie
   float* par;    // [..][2]
@@ -608,8 +616,8 @@ struct GdnLayout {
     table = reinterpret_cast<int*>(take(sizeof(int) * (size_t)(2 + 2 * (size_t)d.N + mc)));
     scal = reinterpret_cast<float*>(take(n * kGdnScal * kC * sizeof(float)));
     frag = reinterpret_cast<T*>(take(n * (bwd ? GdnWs<T>::bwd : GdnWs<T>::fwd) * sizeof(T)));
-    fragT = S0 = Y = dS = D = nullptr;
-    tokf = tokr = end = anc = ancS = par = nullptr;
+    fragT = S0 = Y = dS = D = Yl = nullptr;
+    tokf = tokr = tokb = end = anc = ancS = par = nullptr;
     if (bwd) {
       fragT = reinterpret_cast<T*>(take(n * GdnWs<T>::bwd * sizeof(T)));
       S0 = reinterpret_cast<T*>(take(n * d.K * d.V * sizeof(T)));
@@ -620,6 +628,8 @@ struct GdnLayout {
       tokr = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
       end = reinterpret_cast<float*>(take((size_t)d.N * d.HV * (d.V / 16) * sizeof(float)));
       if (GdnWs<T>::kScanGate) {
+        Yl = reinterpret_cast<T*>(take(n * kC * d.V * sizeof(T)));
+        tokb = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
         const size_t na = (size_t)(mc / kGdnAnchor + 1) * d.HV;
         anc = reinterpret_cast<float*>(take(na * (d.V / 16) * sizeof(float)));
         ancS = reinterpret_cast<float*>(take(na * d.K * d.V * sizeof(float)));

@@ -333,7 +333,8 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
                 int T_, int H, int HV, const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag,
                 int write_final, bf16* __restrict__ o, float* ht, const bf16* __restrict__ dO,
                 const float* __restrict__ dht, bf16* __restrict__ ws_S0, bf16* __restrict__ ws_Y,
-                float* __restrict__ ws_tok, float* __restrict__ ws_end, float* __restrict__ ws_anc) {
+                float* __restrict__ ws_tok, float* __restrict__ ws_end, float* __restrict__ ws_anc,
+                bf16* __restrict__ ws_Yl) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   using L_ = GdnScanLds<K, NP, BWD>;
   using TT = TokTile<bf16, K>;
@@ -549,7 +550,7 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
   }
 
   if constexpr (BWD) {
-    if (role == 2) {  // S0 (its high part) and Y of the chunk behind
+    if (role == 2) {  // S0 (its high part) and Y (both parts) of the chunk behind
       __syncthreads();
       for (int it = 0; it <= nc; ++it) {
         __syncthreads();
@@ -568,7 +569,12 @@ gdn_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const bf
           op_st(ws_S0 + chunk(it - 1) * K * V, r, col0 >> 4, V / 32,
                 (r & 1) ? make_uint2(s0[r >> 1].z, s0[r >> 1].w) : make_uint2(s0[r >> 1].x, s0[r >> 1].y));
 #pragma unroll
-        for (int t = 0; t < 4; ++t) op_st(ws_Y + chunk(it - 1) * kC * V, t, col0 >> 4, V / 32, pack4(x[t]));
+        for (int t = 0; t < 4; ++t) {
+          const uint2 y = pack4(x[t]);
+          op_st(ws_Y + chunk(it - 1) * kC * V, t, col0 >> 4, V / 32, y);
+          reinterpret_cast<uint2*>(ws_Yl)[((chunk(it - 1) * (V / 16) + (col0 >> 4)) * 4 + t) * 64 + lane] =
+              make_uint2(pack2_rest(x[t][0], x[t][1], y.x), pack2_rest(x[t][2], x[t][3], y.y));
+        }
       }
       return;
     }
@@ -931,7 +937,7 @@ static hipError_t scan_t(const kda_dims& d, const GdnCall& c, const GdnLayout<bf
   hipLaunchKernelGGL((gdn_scan_kernel<K, V, NP, BWD>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
                      dim3((BWD ? 256 : 128) * NP), lds, s, (const bf16*)c.q, (const bf16*)c.k, (const bf16*)c.v, c.h0, c.cu,
                      w.table, d.N, d.T, d.H, d.HV, w.scal, w.frag, c.ht != nullptr, (bf16*)c.o, c.ht,
-                     (const bf16*)c.dO, c.dht, w.S0, w.Y, w.tokf, w.end, w.ancS);
+                     (const bf16*)c.dO, c.dht, w.S0, w.Y, w.tokf, w.end, w.ancS, w.Yl);
   return hipGetLastError();
 }
 template <int K, int V, int NP, bool BWD>

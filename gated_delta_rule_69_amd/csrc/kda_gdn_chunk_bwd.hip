@@ -87,7 +87,8 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
                     const int* __restrict__ table, int N, int T_, int H, int HV,
                     const float* __restrict__ ws_scal, const bf16* __restrict__ ws_frag, bf16* __restrict__ dv,
                     float* __restrict__ dh0, bf16* __restrict__ ws_dS, bf16* __restrict__ ws_D,
-                    float* __restrict__ ws_tok, const float* __restrict__ ws_ancS, float* __restrict__ ws_anc) {
+                    float* __restrict__ ws_tok, const float* __restrict__ ws_ancS, float* __restrict__ ws_anc,
+                    const bf16* __restrict__ ws_Y, const bf16* __restrict__ ws_Yl, float* __restrict__ ws_tokb) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   using L_ = GdnRevLds<K, NP>;
   using TT = TokTile<bf16, K>;
@@ -385,6 +386,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
 
   // ---- behind wave
   TileRaw<bf16> vb[4], db[4];  // v and dO of the chunk behind, fetched a round early
+  uint2 yh[4], yl[4];          // Y
   float bw[4][4], pw[4][4];
   auto fetch_b = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
@@ -394,6 +396,8 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
       const float* f = ws_scal + chunk(c) * (kGdnScal * kC);
       lds4(f + kSb * kC + perm_row4(t, g), bw[t]);
       lds4(f + kSp * kC + perm_row4(t, g), pw[t]);
+      yh[t] = op_tile_ld(ws_Y + chunk(c) * kC * V, t, col0 >> 4, V / 32);
+      yl[t] = reinterpret_cast<const uint2*>(ws_Yl)[((chunk(c) * (V / 16) + (col0 >> 4)) * 4 + t) * 64 + lane];
     }
   };
   fetch_b(nc - 1);
@@ -412,18 +416,21 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     __syncthreads();
     if (cb >= nc) continue;
     f32x4 dd[4];
-    float4 sv[4];
+    float4 sv[4], sb[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const f32x4 vt = tile_get(vb[t]), dt = tile_get(db[t]);
-      float z[4];
+      const f32x4 y0 = unpack4(quad_transpose(yh[t])), y1 = unpack4(yl[t]);
+      float z[4], y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         z[e] = row16_sum(bw[t][e] * x[t][e] * vt[e]);
         x[t][e] = fmaf(pw[t][e], dt[e], x[t][e]);
         dd[t][e] = x[t][e] * bw[t][e];
+        y[e] = row16_sum(fmaf(x[t][e], y0[e], x[t][e] * y1[e]));
       }
       sv[t] = make_float4(z[0], z[1], z[2], z[3]);
+      sb[t] = make_float4(y[0], y[1], y[2], y[3]);
     }
     stage();
     if (c >= 0) fetch_b(c);
@@ -437,10 +444,14 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
       op_st(ws_D + chunk(cb) * kC * V, t, col0 >> 4, V / 32, pack4(x[t]));
       tile_st(dv + vrow(cb), HV * V, perm_row4(t, g), col0, tokens(cb), dd[t]);
     }
-    float* tk = ws_tok + (chunk(cb) * (V / 16) + (col0 >> 4)) * kC;
+    const size_t tk = (chunk(cb) * (V / 16) + (col0 >> 4)) * kC;
+    if (l16 == 0) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (l16 == 0) *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = sv[t];
+      for (int t = 0; t < 4; ++t) {
+        *reinterpret_cast<float4*>(ws_tok + tk + perm_row4(t, g)) = sv[t];
+        *reinterpret_cast<float4*>(ws_tokb + tk + perm_row4(t, g)) = sb[t];
+      }
+    }
   }
 }
 
@@ -452,8 +463,8 @@ template <int V>
 __global__ void __launch_bounds__(64 * kGdnAnchor)
 gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __restrict__ table, int T_, int HV,
                     int has_h0, int has_dht, const float* __restrict__ tokf, const float* __restrict__ tokr,
-                    const float* __restrict__ ends, const float* __restrict__ anc, void* __restrict__ dgate,
-                    float* __restrict__ par) {
+                    const float* __restrict__ tokb, const float* __restrict__ ends, const float* __restrict__ anc,
+                    void* __restrict__ dgate, bf16* __restrict__ dbeta, float* __restrict__ par) {
   constexpr int NB = V / 16;
   __shared__ double s_tot[2][kGdnAnchor];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -473,8 +484,12 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
     const size_t at = (size_t)((c0 + cl) * HV + hv) * NB * kC + lane;
     const int64_t tok = (bos + min(cl * kC + lane, len - 1)) * HV + hv;
     double s = 0.;
+    float y = 0.f;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) s += (double)tokf[at + i * kC] - (double)tokr[at + i * kC];
+    for (int i = 0; i < NB; ++i) {
+      s += (double)tokf[at + i * kC] - (double)tokr[at + i * kC];
+      y += tokb[at + i * kC];
+    }
     if (!ok) s = 0.;
     const bool last = (m + 1) * kGdnAnchor >= nc;
     const float* e = last ? ends + ((size_t)n * HV + hv) * NB
@@ -498,7 +513,10 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
     // before a sequence's first token there is nothing to decay without a state
     const float dg = c == 0 && lane == 0 && !has_h0 ? 0.f : (float)(s + behind);
     const float dx = gate.raw ? -dg * as * sigmoid_f32(xb) : dg;
-    if (ok) st_any(dgate, tok, gate.bf, dx);
+    if (ok) {
+      st_any(dgate, tok, gate.bf, dx);
+      dbeta[tok] = from_f32<bf16>(y);
+    }
     if (gate.A_log || gate.dt_bias) {
       float pa = ok ? dg * gn : 0.f, pb = ok ? dx : 0.f;  // dg / dA_log = g
 #pragma unroll
@@ -672,8 +690,8 @@ __device__ __forceinline__ float op_dot(const Op8<T>& a, const Op8<T>& b) {
 
 // bf16. Eight waves: wave w and wave w + 4 own token tile w. The first four
 // form what takes a token as the later of a pair (from S0, Y: dq and a part of
-// dk), the others what takes it as the earlier (from dS, dO, D: dbeta and the
-// rest of dk). The kernel moves 180 KB for some 2 us of products, so one
+// dk), the others what takes it as the earlier (from dS, dO, D: the rest
+// of dk). The kernel moves 180 KB for some 2 us of products, so one
 // workgroup stays on a CU, walks its (chunk, head) items and keeps two sets of
 // transfers into LDS going: S0, dS, k and q arrive while the 64 x 64 products
 // run over Y, D and dO, and the next item's Y, D and dO while the channel tiles
@@ -694,7 +712,7 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
                  const int32_t* __restrict__ cu, const int* __restrict__ table, int chunks, int N, int T_, int H,
                  int HV, int l2, float scale, const float* __restrict__ ws_scal, const bf16* __restrict__ ws_S0,
                  const bf16* __restrict__ ws_Y, const bf16* __restrict__ ws_dS, const bf16* __restrict__ ws_D,
-                 bf16* __restrict__ dq, bf16* __restrict__ dk, bf16* __restrict__ dbeta) {
+                 bf16* __restrict__ dq, bf16* __restrict__ dk) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   using L_ = GdnLocalLds<K, V>;
   using TT = TokTile<bf16, K>;
@@ -818,17 +836,8 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
           stage();
         }
       } else {
-        float x = 0.f;
 #pragma unroll
-        for (int u = 0; u < NV; ++u) {
-          op_ld(oa[u], sY, wave, u, NV, lane);
-          Op8<bf16> d;
-          op_ld(d, sD, wave, u, NV, lane);
-          x += op_dot(d, oa[u]);
-        }
-        x += __shfl_xor(x, 16);
-        x += __shfl_xor(x, 32);
-        if (g == 0 && own < L) dbeta[(t0 + own) * HV + hv] = from_f32<bf16>(x);  // <D_i, Y_i>
+        for (int u = 0; u < NV; ++u) op_ld(oa[u], sY, wave, u, NV, lane);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           f32x4 w[2], z[2];
@@ -1342,7 +1351,8 @@ static hipError_t rev_t(const kda_dims& d, const void* q, const void* k, const v
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((gdn_rev_scan_kernel<K, V, NP>), dim3(scan_grid((int64_t)d.N * d.HV, V, 16 * NP)),
                      dim3(256 * NP), lds, s, (const bf16*)q, (const bf16*)k, (const bf16*)v, (const bf16*)dO, dht,
-                     cu, w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (bf16*)dv, dh0, w.dS, w.D, w.tokr, w.ancS, w.anc);
+                     cu, w.table, d.N, d.T, d.H, d.HV, w.scal, w.fragT, (bf16*)dv, dh0, w.dS, w.D, w.tokr, w.ancS, w.anc, w.Y,
+                     w.Yl, w.tokb);
   return hipGetLastError();
 }
 template <int K, int V, int NP>
@@ -1368,7 +1378,8 @@ static hipError_t local_t(const kda_dims& d, const void* q, const void* k, const
   const int64_t chains = (int64_t)d.N * d.HV, segs = (cu ? mc : mc / d.N) / kGdnAnchor + 1;
   const int64_t ny = std::min<int64_t>(segs, std::max<int64_t>(1, 4 * kda_host::device_cus() / chains));
   hipLaunchKernelGGL((gdn_gate_bwd_kernel<V>), dim3((unsigned)chains, (unsigned)ny), dim3(64 * kGdnAnchor), 0, s, gate,
-                     cu, w.table, d.T, d.HV, has_h0, has_dht, w.tokf, w.tokr, w.end, w.anc, dgate, w.par);
+                     cu, w.table, d.T, d.HV, has_h0, has_dht, w.tokf, w.tokr, w.tokb, w.end, w.anc, dgate,
+                     (bf16*)dbeta, w.par);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr size_t lds = GdnLocalLds<K, V>::total;
@@ -1379,7 +1390,7 @@ static hipError_t local_t(const kda_dims& d, const void* q, const void* k, const
   const int64_t wgs = std::min<int64_t>(mc * d.H, kda_host::device_cus());
   hipLaunchKernelGGL((gdn_local_kernel<K, V>), dim3((unsigned)wgs), dim3(512), lds, s, (const bf16*)q, (const bf16*)k,
                      (const bf16*)dO, cu, w.table, (int)mc, d.N, d.T, d.H, d.HV, l2, 1.0f / sqrtf((float)K), w.scal,
-                     w.S0, w.Y, w.dS, w.D, (bf16*)dq, (bf16*)dk, (bf16*)dbeta);
+                     w.S0, w.Y, w.dS, w.D, (bf16*)dq, (bf16*)dk);
   return hipGetLastError();
 }
 template <int K, int V>
