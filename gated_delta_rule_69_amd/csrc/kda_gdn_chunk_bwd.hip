@@ -1,16 +1,16 @@
 // Chunked gated delta rule with a scalar gate, backward. Formulas, layouts and
 // the rounding rule are in kda_gdn.h.
 //
-//   gdn_rev_scan_kernel   one wave per 16 columns of one (sequence, value head)
-//                         state gradient, walking the chunks backwards; writes
-//                         dv, its part of the tokens' scalars, and per chunk dS
-//                         (at the chunk's end) and D.
-//   gdn_gate_bwd_kernel   bf16: the gate's gradient from the tokens' scalars,
-//                         a workgroup per anchor.
-//   gdn_local_kernel      per (chunk, q/k head): dq, dk (summed over the head's
-//                         value heads) and dbeta from the chunk's S0, Y, dS and
-//                         D (gdn_local32_kernel for FP32 inputs, with the gate's
-//                         gradient).
+//   gdn_rev_scan_kernel   the state gradient of 16 columns of one (sequence,
+//                         value head), walking the chunks backwards; writes
+//                         dv, its part of the tokens' scalars, <D, Y>, and per
+//                         chunk dS (at the chunk's end) and D.
+//   gdn_gate_bwd_kernel   bf16: the gate's gradient and dbeta from the tokens'
+//                         scalars, a workgroup per anchor.
+//   gdn_local_kernel      per (chunk, q/k head): dq and dk (summed over the head's
+//                         value heads) from the chunk's S0, Y, dS and D
+//                         (gdn_local32_kernel for FP32 inputs, with dbeta and the
+//                         gate's gradient).
 //   gdn_par_kernel        dA_log and d_dt_bias from per-chunk partial sums.
 //
 // With dP = dO Delta^T and dE = E Delta^T (64 x 64) the gradients of k, q are
@@ -18,7 +18,11 @@
 //   dk  = e^{G_last - G} (Delta dS^T) - e^G (E S0^T)
 //         + (e . dP)^T q~ - (e . dE) K - (e . dE)^T K         (dE strictly lower)
 // S0, Y, dS and D pass between the kernels rounded to the inputs' type: they
-// feed dq, dk and dbeta, which are rounded to it as well.
+// feed dq and dk, which are rounded to it as well and sum over V or 64 tokens.
+// dbeta = <D, Y> is one number per token: from rounded operands its error does
+// not shrink where the sum's terms cancel (5e-3 in a call of a few tokens), so
+// bf16 takes it from D in FP32 and Y's two parts inside the reverse scan (252 ->
+// 275 us at 64 chains of 4096 tokens).
 //
 // The gate's gradient comes one of two ways.
 //   bf16: dg_t = <S_T, dS_T> + sum_{t <= i < T} s_i (kda_gdn.h), from FP32 values
@@ -43,19 +47,20 @@
 namespace kda {
 
 // ------------------------------------------------------------------ reverse scan
-// bf16. Three waves per 16 columns. The state wave keeps dS and walks
+// bf16. Four waves per 16 columns. The state wave keeps dS and walks
 //   x = e^{G_last - G} k dS + p,  D' = x - M^T b (x + P_ii dO),  D = D' + P_ii dO,
 //   dS = e^{G_last} dS + Z - (e^G k)^T b D
 // with p = P^T dO (P strictly lower) and Z = (e^G q~)^T dO, which do not depend
 // on dS: the ahead wave forms them a chunk early, and issues the transfers of
 // left operands into LDS. The behind wave follows a chunk late with what
 // leaves: dS, D and dv = b D in memory, and the columns' part of the tokens'
-// scalars. (One side wave doing both was the step's longest: 373 us at 64
-// chains.) Two barriers per chunk: at its top (operands, p and Z in LDS), and
-// after the state wave has taken p and Z and the behind wave the previous
-// chunk's dS and D'. Of the workgroup's 4 NP waves NP leave at once: the state
-// waves then have a SIMD each, ahead and behind waves share the others. 64
-// chains of 4096 tokens, K = V = 128: 246 us, 3.8 us a chunk, bound by the step.
+// scalars; a fourth forms <D, Y>. (One side wave doing all was the step's
+// longest: 373 us at 64 chains; <D, Y> in the behind wave 278 us.) Two barriers
+// per chunk: at its top (operands, p and Z in LDS), and after the state wave has
+// taken p and Z and the others the previous chunk's dS and D'. The state waves
+// share their SIMDs with the <D, Y> waves only. 64 chains of 4096 tokens, K = V
+// = 128: 275 us, 4.3 us a chunk, bound by the step; splitting the ahead wave in
+// two (p, Z) took 15 us more.
 template <int K, int NP>
 struct GdnRevLds {
   static constexpr int NK = K / 32, RT = K / 16;
@@ -95,8 +100,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
   constexpr int NK = K / 32, RT = K / 16, BV = 16 * NP, NVB = V / BV;
   const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int pair = wave % NP, role = wave / NP;  // 0 state, 1 ahead, 3 behind
-  if (role == 2) return;
+  const int pair = wave % NP, role = wave / NP;  // 0 state, 1 ahead, 2 dbeta, 3 behind
   const GdnChain ch = gdn_chain(NVB, cu, table, N, T_, H, HV);
   if (!ch.ok) return;
   const int col0 = ch.vb * BV + 16 * pair, hv = ch.hv, len = ch.len;
@@ -384,9 +388,55 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     return;
   }
 
+  if (role == 2) {  // <D, Y> of the chunk behind
+    TileRaw<bf16> db[4];
+    uint2 yh[4], yl[4];
+    float pw[4][4];
+    auto fetch = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        tile_ld(db[t], dO + vrow(c), HV * V, perm_row4(t, g), col0, tokens(c));
+        lds4(ws_scal + chunk(c) * (kGdnScal * kC) + kSp * kC + perm_row4(t, g), pw[t]);
+        yh[t] = op_tile_ld(ws_Y + chunk(c) * kC * V, t, col0 >> 4, V / 32);
+        yl[t] = reinterpret_cast<const uint2*>(ws_Yl)[((chunk(c) * (V / 16) + (col0 >> 4)) * 4 + t) * 64 + lane];
+      }
+    };
+    fetch(nc - 1);
+    __syncthreads();
+    for (int c = nc - 1; c >= -1; --c) {
+      const int cb = c + 1;
+      __syncthreads();
+      f32x4 x[4];
+      if (cb < nc) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) x[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + (t * 64 + lane) * 16);
+      }
+      __syncthreads();
+      if (cb >= nc) continue;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const f32x4 dt = tile_get(db[t]), y0 = unpack4(quad_transpose(yh[t])), y1 = unpack4(yl[t]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float d = fmaf(pw[t][e], dt[e], x[t][e]);
+          x[t][e] = row16_sum(fmaf(d, y0[e], d * y1[e]));
+        }
+      }
+      stage();
+      if (c >= 0) fetch(c);
+      stage();
+      float* tk = ws_tokb + (chunk(cb) * (V / 16) + (col0 >> 4)) * kC;
+      if (l16 == 0) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = make_float4(x[t][0], x[t][1], x[t][2], x[t][3]);
+      }
+    }
+    return;
+  }
+
   // ---- behind wave
   TileRaw<bf16> vb[4], db[4];  // v and dO of the chunk behind, fetched a round early
-  uint2 yh[4], yl[4];          // Y
   float bw[4][4], pw[4][4];
   auto fetch_b = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
@@ -396,8 +446,6 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
       const float* f = ws_scal + chunk(c) * (kGdnScal * kC);
       lds4(f + kSb * kC + perm_row4(t, g), bw[t]);
       lds4(f + kSp * kC + perm_row4(t, g), pw[t]);
-      yh[t] = op_tile_ld(ws_Y + chunk(c) * kC * V, t, col0 >> 4, V / 32);
-      yl[t] = reinterpret_cast<const uint2*>(ws_Yl)[((chunk(c) * (V / 16) + (col0 >> 4)) * 4 + t) * 64 + lane];
     }
   };
   fetch_b(nc - 1);
@@ -416,21 +464,18 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     __syncthreads();
     if (cb >= nc) continue;
     f32x4 dd[4];
-    float4 sv[4], sb[4];
+    float4 sv[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const f32x4 vt = tile_get(vb[t]), dt = tile_get(db[t]);
-      const f32x4 y0 = unpack4(quad_transpose(yh[t])), y1 = unpack4(yl[t]);
-      float z[4], y[4];
+      float z[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         z[e] = row16_sum(bw[t][e] * x[t][e] * vt[e]);
         x[t][e] = fmaf(pw[t][e], dt[e], x[t][e]);
         dd[t][e] = x[t][e] * bw[t][e];
-        y[e] = row16_sum(fmaf(x[t][e], y0[e], x[t][e] * y1[e]));
       }
       sv[t] = make_float4(z[0], z[1], z[2], z[3]);
-      sb[t] = make_float4(y[0], y[1], y[2], y[3]);
     }
     stage();
     if (c >= 0) fetch_b(c);
@@ -449,13 +494,12 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         *reinterpret_cast<float4*>(ws_tok + tk + perm_row4(t, g)) = sv[t];
-        *reinterpret_cast<float4*>(ws_tokb + tk + perm_row4(t, g)) = sb[t];
       }
     }
   }
 }
 
-// bf16: the gate's gradient from the tokens' scalars. A workgroup takes the 16
+// bf16: the gate's gradient and dbeta from the tokens' scalars. A workgroup takes the 16
 // chunks from one anchor to the next, lane = token, wave = chunk; the sums
 // towards the anchor behind them (the sequence's end for the last) are held in
 // double. Grid (chain, y): y strides over a chain's anchors.
