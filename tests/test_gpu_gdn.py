@@ -424,3 +424,20 @@ def test_long_backward_agrees_with_fp32(lens, H, HV, K):
         for m in ("dq", "dk", "dv", "dg", "dbeta", "dA_log", "ddt_bias"):
             e = G.rel(res[0][m], res[1][m].cpu().numpy())
             assert e <= (DV16 if m == "dv" else G16), (seed, m, e)
+
+
+def test_dbeta_of_single_tokens_keeps_its_digits():
+    """One token without a state: dbeta = (q . k / sqrt(K)) <dO, v>, one number
+    that no other averages with. Bound per value: the output's rounding, 2^-8 of
+    it, and 2^-14 of |q . k / sqrt(K)| |dO| |v| (operands in two parts, off by
+    2^-16 each, FP32 sums), which stays where the sum cancels."""
+    for seed in range(8):
+        c = G.make(800 + seed, [1] * 12, K=64, V=128, H=2, HV=4, h0=False)
+        d = G.device(c)
+        r = kda.chunk_gdn_bwd(*G.scan_args(d), d["do"], d["dht"], **G.scan_kw(c, d))
+        q, k, v, do = (c[m].astype(np.float64)[0] for m in ("q", "k", "v", "do"))
+        p = np.repeat((q * k).sum(-1), 2, -1) / np.sqrt(64)
+        ref = p * (do * v).sum(-1)
+        size = np.abs(p) * np.linalg.norm(do, axis=-1) * np.linalg.norm(v, axis=-1)
+        err = np.abs(r["dbeta"][0].double().cpu().numpy() - ref)
+        assert (err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -14 * size).all(), seed
