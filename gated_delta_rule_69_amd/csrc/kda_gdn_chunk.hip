@@ -311,7 +311,8 @@ gdn_intra_kernel(const T* __restrict__ q, const T* __restrict__ k, GdnGate gate,
 // dO comes in: o' is formed in full precision (S0 and P split as well; P is
 // strictly lower) for the tokens' scalars of the gate's gradient. Two output waves
 // per pair take two token tiles each, and a fourth wave stores S0 and Y: 64
-// chains of 4096 tokens 200 us (one output wave 245 us, storing too 261 us).
+// chains of 4096 tokens 207 us (with one output wave 45 us more, and 60 where it
+// stores too).
 template <int K, int NP, bool BWD>
 struct GdnScanLds {
   static constexpr int NK = K / 32, PT = BWD ? 2 : 1;

@@ -59,7 +59,7 @@ namespace kda {
 // per chunk: at its top (operands, p and Z in LDS), and after the state wave has
 // taken p and Z and the others the previous chunk's dS and D'. The state waves
 // share their SIMDs with the <D, Y> waves only. 64 chains of 4096 tokens, K = V
-// = 128: 275 us, 4.3 us a chunk, bound by the step; splitting the ahead wave in
+// = 128: 272 us, 4.3 us a chunk, bound by the step; splitting the ahead wave in
 // two (p, Z) took 15 us more.
 template <int K, int NP>
 struct GdnRevLds {
@@ -739,7 +739,7 @@ __device__ __forceinline__ float op_dot(const Op8<T>& a, const Op8<T>& b) {
 // workgroup stays on a CU, walks its (chunk, head) items and keeps two sets of
 // transfers into LDS going: S0, dS, k and q arrive while the 64 x 64 products
 // run over Y, D and dO, and the next item's Y, D and dO while the channel tiles
-// run over S0 and dS. 4096 items of K = V = 128, 720 MB: 175 us, 4.1 TB/s (305 us
+// run over S0 and dS. 4096 items of K = V = 128, 720 MB: 170 us, 4.2 TB/s (305 us
 // with four waves a workgroup loading their operands where they use them).
 template <int K, int V>
 struct GdnLocalLds {
