@@ -65,6 +65,7 @@ constexpr int kTriElems = 6 * kFragElems;   // one triangular matrix
 enum GdnScal : int {
   kSk = 0,   // e^G rk                 (rk, rq: 1, or the inverse L2 norms of k and q rows)
   kSeb = 1,  // e^{G_last - G} rk b
+  kSpy = 1,  // bf16 backward, behind the scans: <dO_i, Y_i>
   kSl = 2,   // e^{G_last}, 64 times
   kSb = 3,   // b
   kSq = 4,   // e^G rq / sqrt(K)
@@ -598,7 +599,7 @@ struct GdnLayout {
   float* tokf;   // [..][V / 16][64]: the tokens' scalars from the forward run, per 16 columns
   float* tokr;   // [..][V / 16][64]: those from the reverse scan
   float* end;    // [N * HV][V / 16]: <S_T, dS_T> of the columns
-  float* tokb;   // [..][V / 16][64]: <D, Y>
+  float* tokb;   // [..][2][V / 16][64]: <D, Y>, <dO, Y>
   float* anc;    // [anchors * HV][V / 16]: <S, dS> of the columns before an anchor chunk
   float* ancS;   // [anchors * HV][V / 16][K / 16][64][4]: S there in FP32, as the accumulators lie
   float* par;    // [..][2]
@@ -629,7 +630,7 @@ struct GdnLayout {
       end = reinterpret_cast<float*>(take((size_t)d.N * d.HV * (d.V / 16) * sizeof(float)));
       if (GdnWs<T>::kScanGate) {
         Yl = reinterpret_cast<T*>(take(n * kC * d.V * sizeof(T)));
-        tokb = reinterpret_cast<float*>(take(n * (d.V / 16) * kC * sizeof(float)));
+        tokb = reinterpret_cast<float*>(take(2 * n * (d.V / 16) * kC * sizeof(float)));
         const size_t na = (size_t)(mc / kGdnAnchor + 1) * d.HV;
         anc = reinterpret_cast<float*>(take(na * (d.V / 16) * sizeof(float)));
         ancS = reinterpret_cast<float*>(take(na * d.K * d.V * sizeof(float)));

@@ -19,7 +19,7 @@
 //         + (e . dP)^T q~ - (e . dE) K - (e . dE)^T K         (dE strictly lower)
 // S0, Y, dS and D pass between the kernels rounded to the inputs' type: they
 // feed dq and dk, which are rounded to it as well and sum over V or 64 tokens.
-// dbeta = <D, Y> is one number per token: from rounded operands its error does
+// dbeta = <D, Y> (and <dO, Y>, which scales a token's own part of dq and dk) is one number per token: from rounded operands its error does
 // not shrink where the sum's terms cancel (5e-3 in a call of a few tokens), so
 // bf16 takes it from D in FP32 and Y's two parts inside the reverse scan (252 ->
 // 275 us at 64 chains of 4096 tokens).
@@ -388,7 +388,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     return;
   }
 
-  if (role == 2) {  // <D, Y> of the chunk behind
+  if (role == 2) {  // <D, Y> and <dO, Y> of the chunk behind
     TileRaw<bf16> db[4];
     uint2 yh[4], yl[4];
     float pw[4][4];
@@ -406,7 +406,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
     for (int c = nc - 1; c >= -1; --c) {
       const int cb = c + 1;
       __syncthreads();
-      f32x4 x[4];
+      f32x4 x[4], z[4];
       if (cb < nc) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) x[t] = *reinterpret_cast<const f32x4*>(xch + L_::xS + (t * 64 + lane) * 16);
@@ -420,16 +420,20 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
         for (int e = 0; e < 4; ++e) {
           const float d = fmaf(pw[t][e], dt[e], x[t][e]);
           x[t][e] = row16_sum(fmaf(d, y0[e], d * y1[e]));
+          z[t][e] = row16_sum(fmaf(dt[e], y0[e], dt[e] * y1[e]));
         }
       }
       stage();
       if (c >= 0) fetch(c);
       stage();
-      float* tk = ws_tokb + (chunk(cb) * (V / 16) + (col0 >> 4)) * kC;
+      float* tk = ws_tokb + (chunk(cb) * 2 * (V / 16) + (col0 >> 4)) * kC;
       if (l16 == 0) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) {
           *reinterpret_cast<float4*>(tk + perm_row4(t, g)) = make_float4(x[t][0], x[t][1], x[t][2], x[t][3]);
+          *reinterpret_cast<float4*>(tk + (V / 16) * kC + perm_row4(t, g)) =
+              make_float4(z[t][0], z[t][1], z[t][2], z[t][3]);
+        }
       }
     }
     return;
@@ -508,7 +512,8 @@ __global__ void __launch_bounds__(64 * kGdnAnchor)
 gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __restrict__ table, int T_, int HV,
                     int has_h0, int has_dht, const float* __restrict__ tokf, const float* __restrict__ tokr,
                     const float* __restrict__ tokb, const float* __restrict__ ends, const float* __restrict__ anc,
-                    void* __restrict__ dgate, bf16* __restrict__ dbeta, float* __restrict__ par) {
+                    void* __restrict__ dgate, bf16* __restrict__ dbeta, float* __restrict__ par,
+                    float* __restrict__ ws_scal) {
   constexpr int NB = V / 16;
   __shared__ double s_tot[2][kGdnAnchor];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -528,11 +533,13 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
     const size_t at = (size_t)((c0 + cl) * HV + hv) * NB * kC + lane;
     const int64_t tok = (bos + min(cl * kC + lane, len - 1)) * HV + hv;
     double s = 0.;
-    float y = 0.f;
+    float y = 0.f, p = 0.f;
+    const size_t atb = (size_t)((c0 + cl) * HV + hv) * 2 * NB * kC + lane;
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       s += (double)tokf[at + i * kC] - (double)tokr[at + i * kC];
-      y += tokb[at + i * kC];
+      y += tokb[atb + i * kC];
+      p += tokb[atb + (NB + i) * kC];
     }
     if (!ok) s = 0.;
     const bool last = (m + 1) * kGdnAnchor >= nc;
@@ -554,6 +561,8 @@ gdn_gate_bwd_kernel(GdnGate gate, const int32_t* __restrict__ cu, const int* __r
 #pragma unroll
     for (int w = kGdnAnchor - 1; w > 0; --w) behind += w > wave ? s_tot[b][w] : 0.;
     if (c >= nc) continue;
+    // the scans are done with this slot
+    ws_scal[(size_t)((c0 + c) * HV + hv) * (kGdnScal * kC) + kSpy * kC + lane] = ok ? p : 0.f;
     // before a sequence's first token there is nothing to decay without a state
     const float dg = c == 0 && lane == 0 && !has_h0 ? 0.f : (float)(s + behind);
     const float dx = gate.raw ? -dg * as * sigmoid_f32(xb) : dg;
@@ -829,10 +838,11 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
       // Z_ij = - e_ij b_i b_j rk_j D_i.Y_j, from the products with Y's rows on the left, so the
       // accumulators are the operand with the wave's tokens as rows. As columns (contraction
       // over i): W'_ij = e_ij b_j rq_i / sqrt(K) dO_i.Y_j, Z'_ij = - e_ij b_i b_j rk_i D_i.Y_j.
+      // dO_i.Y_i comes from the scan in FP32: a token on its own has all of dq and dk from it.
       Op8<bf16> oa[NV], ob[NV];  // own rows: dO and D; Y
       Op8<bf16> wo[2], zo[2];
       const double Go = sG[own];
-      const float bo = sc[kSb * kC + own];
+      const float bo = sc[kSb * kC + own], pyo = sc[kSpy * kC + own];
       if (later) {
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
@@ -870,7 +880,7 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
               for (int e = 0; e < 4; ++e) {
                 const int o = row4 + e;  // the earlier token
                 const float ej = ex2((own >= o) & (own < L) ? gg[e] : -INFINITY) * b4[e] * rk_[e];
-                w[i][e] *= ej * scale;
+                w[i][e] = (own == o ? pyo : w[i][e]) * (ej * scale);
                 z[i][e] *= own > o ? -ej * bo : 0.f;
               }
             }
@@ -915,7 +925,7 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
               for (int e = 0; e < 4; ++e) {
                 const int o = row4 + e;  // the later token
                 const float ei = ex2((o >= own) & (o < L) ? -gg[e] : -INFINITY) * bo;
-                w[i][e] *= ei * rq_[e] * scale;
+                w[i][e] = (own == o ? pyo : w[i][e]) * (ei * rq_[e] * scale);
                 z[i][e] *= o > own ? -ei * b4[e] * rk_[e] : 0.f;
               }
             }
@@ -1423,7 +1433,7 @@ static hipError_t local_t(const kda_dims& d, const void* q, const void* k, const
   const int64_t ny = std::min<int64_t>(segs, std::max<int64_t>(1, 4 * kda_host::device_cus() / chains));
   hipLaunchKernelGGL((gdn_gate_bwd_kernel<V>), dim3((unsigned)chains, (unsigned)ny), dim3(64 * kGdnAnchor), 0, s, gate,
                      cu, w.table, d.T, d.HV, has_h0, has_dht, w.tokf, w.tokr, w.tokb, w.end, w.anc, dgate,
-                     (bf16*)dbeta, w.par);
+                     (bf16*)dbeta, w.par, w.scal);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   constexpr size_t lds = GdnLocalLds<K, V>::total;

@@ -441,3 +441,24 @@ def test_dbeta_of_single_tokens_keeps_its_digits():
         size = np.abs(p) * np.linalg.norm(do, axis=-1) * np.linalg.norm(v, axis=-1)
         err = np.abs(r["dbeta"][0].double().cpu().numpy() - ref)
         assert (err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -14 * size).all(), seed
+
+
+def test_dq_dk_of_single_tokens_keep_their_digits():
+    """One token without a state: dq = s k and dk = s q with s = beta <dO, v> /
+    sqrt(K), one number for all of a row. Bound per element: the output's
+    rounding (2^-8 of it), s as a product's operand (2^-8 of each value head's
+    term) and 2^-14 of beta |dO| |v| / sqrt(K) |k_c|, which stays where the sum
+    in s cancels."""
+    for seed in range(8):
+        c = G.make(820 + seed, [1] * 12, K=64, V=128, H=2, HV=4, h0=False)
+        d = G.device(c)
+        r = kda.chunk_gdn_bwd(*G.scan_args(d), d["do"], d["dht"], **G.scan_kw(c, d))
+        q, k, v, do, b = (c[m].astype(np.float64)[0] for m in ("q", "k", "v", "do", "beta"))
+        s = b * (do * v).sum(-1) / 8
+        size = b * np.linalg.norm(do, axis=-1) * np.linalg.norm(v, axis=-1) / 8
+        per = lambda a: a.reshape(12, 2, 2).sum(-1)[..., None]  # noqa: E731  value heads of a q/k head
+        for m, x in (("dq", k), ("dk", q)):
+            ref = per(s) * x
+            err = np.abs(r[m][0].double().cpu().numpy() - ref)
+            tol = 2.0 ** -8 * (np.abs(ref) + per(np.abs(s)) * np.abs(x)) + 2.0 ** -14 * per(size) * np.abs(x)
+            assert (err <= tol).all(), (seed, m)
