@@ -602,8 +602,7 @@ kda_status kda_gdn_recurrent_fwd(const kda_dims* dims, kda_dtype dtype, const vo
                                  float* final_state, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------
- * Output norm of the layer (FusedRMSNormGated in the pages' layer imports, and
- * its layer-norm form), over rows of D:
+ * Output norm of the layer, over rows of D:
  *   mu = mean(x) (KDA_NORM_LAYER; 0 for KDA_NORM_RMS)
  *   n = (x - mu) / sqrt(mean((x - mu)^2) + eps),  a = n * weight + bias
  *   y = a * act(gate)      (y = a without a gate)
