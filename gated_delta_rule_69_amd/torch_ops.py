@@ -35,6 +35,11 @@ only; every step runs in libkda's kernels).
   torch.ops.kda.gated_norm(x, weight, bias, gate, cu_seqlens, kind, activation, eps) -> y
       The output norm, differentiable in x, weight, bias and gate.
 
+Capturing a backward pass in a graph: as with any autograd operator, capture
+forward and backward together, with no eager graph of the same leaves alive
+(its gradient accumulation runs on the stream it was made on, outside the
+capture). chunk_gdn_bwd and gated_norm_bwd themselves can be captured at any time.
+
 All have fake (meta) implementations, so they trace under torch.compile and
 FakeTensor. Shapes: q, k [B, T, H, K]; v [B, T, HV, V]; x [B, T, HV, K] FP32;
 beta [B, T, HV]; A_log [HV] FP32; dt_bias [HV, K] FP32; initial_state
