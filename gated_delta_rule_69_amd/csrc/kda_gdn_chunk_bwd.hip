@@ -733,6 +733,11 @@ gdn_rev_scan32_kernel(const float* __restrict__ q, const float* __restrict__ k, 
 }
 
 // ------------------------------------------------------------------ local gradients
+// c += a b, the left operand split
+__device__ __forceinline__ f32x4 mma8a(const Op8s<bf16>& a, const Op8<bf16>& b, f32x4 c) {
+  c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.lo, b.v, c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.hi, b.v, c, 0, 0, 0);
+}
 template <typename T>
 __device__ __forceinline__ float op_dot(const Op8<T>& a, const Op8<T>& b) {
   float s = 0.f;
@@ -748,8 +753,10 @@ __device__ __forceinline__ float op_dot(const Op8<T>& a, const Op8<T>& b) {
 // workgroup stays on a CU, walks its (chunk, head) items and keeps two sets of
 // transfers into LDS going: S0, dS, k and q arrive while the 64 x 64 products
 // run over Y, D and dO, and the next item's Y, D and dO while the channel tiles
-// run over S0 and dS. 4096 items of K = V = 128, 720 MB: 170 us, 4.2 TB/s (305 us
-// with four waves a workgroup loading their operands where they use them).
+// run over S0 and dS. 4096 items of K = V = 128, 720 MB: 173 us, 4.2 TB/s (305 us
+// with four waves a workgroup loading their operands where they use them; 166 us
+// with the pairs' factors W and Z rounded to one part, which left a call of three
+// tokens 5e-3 off).
 template <int K, int V>
 struct GdnLocalLds {
   static constexpr uint32_t tok = TokTile<bf16, K>::bytes, st = K * V * sizeof(bf16), row = kC * V * sizeof(bf16);
@@ -840,7 +847,7 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
       // over i): W'_ij = e_ij b_j rq_i / sqrt(K) dO_i.Y_j, Z'_ij = - e_ij b_i b_j rk_i D_i.Y_j.
       // dO_i.Y_i comes from the scan in FP32: a token on its own has all of dq and dk from it.
       Op8<bf16> oa[NV], ob[NV];  // own rows: dO and D; Y
-      Op8<bf16> wo[2], zo[2];
+      Op8s<bf16> wo[2], zo[2];  // in two parts: one number scales a pair's whole row of k or q
       const double Go = sG[own];
       const float bo = sc[kSb * kC + own], pyo = sc[kSpy * kC + own];
       if (later) {
@@ -974,8 +981,8 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
           for (int s = 0; s < 2; ++s) {
             Op8<bf16> kc;
             TT::cols(kc, sK, r, s, lane);
-            tq = mma8(wo[s], kc, tq);
-            tr = mma8(zo[s], kc, tr);
+            tq = mma8a(wo[s], kc, tq);
+            tr = mma8a(zo[s], kc, tr);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -1003,8 +1010,8 @@ gdn_local_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, const b
             Op8<bf16> kc, qc;
             TT::cols(kc, sK, r, s, lane);
             TT::cols(qc, sQ, r, s, lane);
-            tc = mma8(wo[s], qc, tc);
-            tc = mma8(zo[s], kc, tc);
+            tc = mma8a(wo[s], qc, tc);
+            tc = mma8a(zo[s], kc, tc);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) ak[r][e] += a3[e] * fe[e] + frk[e] * tc[e];
