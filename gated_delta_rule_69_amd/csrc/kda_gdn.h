@@ -580,9 +580,9 @@ namespace kda {
 // Workspace of a chunked call, in order: the varlen chunk table, then per
 // (chunk, value head): row factors and fragments, and for the backward S0, Y,
 // dS, D, the per-token scalars of each 16 columns and the gate-parameter partials.
-constexpr int kGdnAnchor = 16;  // chunks between a sequence's anchors of the gate's gradient
+constexpr int kGdnAnchor = 8;  // chunks between a sequence's anchors of the gate's gradient
 // A chunk c of a sequence that starts at flat chunk c0 and has an anchor: its
-// slot (anchors are 16 chunks apart and a sequence's first chunk has none, so
+// slot (anchors are kGdnAnchor chunks apart and a sequence's first chunk has none, so
 // no two share one).
 __host__ __device__ __forceinline__ size_t gdn_anchor(int64_t c0, int c) { return (size_t)((c0 + c) / kGdnAnchor); }
 template <typename T>

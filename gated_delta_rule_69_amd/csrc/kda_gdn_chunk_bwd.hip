@@ -31,9 +31,10 @@
 //     tokens of either sign, by 1e-2 and more. A token's scalars are off by some
 //     1e-6, adding up like a random walk towards T, the same for all tokens
 //     before: with T the sequence's end dA_log was off by 5e-3 at 4096 tokens
-//     and 4e-2 at 16384. T is therefore the next anchor: every 16 chunks the
-//     forward run keeps S in FP32 and the reverse scan takes <S, dS> there (3%
-//     of the workspace).
+//     and 4e-2 at 16384. T is therefore the next anchor: every 8 chunks the
+//     forward run keeps S in FP32 and the reverse scan takes <S, dS> there (6%
+//     of the workspace; 64 chains of 4096 tokens 24 us in all). Every 16 chunks is
+//     12 us cheaper and left 3e-3 beside the outputs' rounding.
 //   FP32: the operands are exact, the walk would not be small enough, and dg is
 //     taken chunk by chunk: what the decay between tokens t - 1 and t scales is
 //     the rows i >= t against S0, the columns j < t towards the chunk's end and
@@ -59,7 +60,7 @@ namespace kda {
 // per chunk: at its top (operands, p and Z in LDS), and after the state wave has
 // taken p and Z and the others the previous chunk's dS and D'. The state waves
 // share their SIMDs with the <D, Y> waves only. 64 chains of 4096 tokens, K = V
-// = 128: 272 us, 4.3 us a chunk, bound by the step; splitting the ahead wave in
+// = 128: 281 us, 4.4 us a chunk, bound by the step; splitting the ahead wave in
 // two (p, Z) took 15 us more.
 template <int K, int NP>
 struct GdnRevLds {
@@ -503,7 +504,7 @@ gdn_rev_scan_kernel(const bf16* __restrict__ q, const bf16* __restrict__ k, cons
   }
 }
 
-// bf16: the gate's gradient and dbeta from the tokens' scalars. A workgroup takes the 16
+// bf16: the gate's gradient and dbeta from the tokens' scalars. A workgroup takes the 8
 // chunks from one anchor to the next, lane = token, wave = chunk; the sums
 // towards the anchor behind them (the sequence's end for the last) are held in
 // double. Grid (chain, y): y strides over a chain's anchors.
